@@ -63,7 +63,9 @@
  *    pa_decode_fp8, pa_decode_fp8_rows (+ its workspace size),
  *    pa_decode_shared_prefix_fp8 (+ its workspace size),
  *    pa_swap_blocks, pa_decode_noalloc (+
- *    pa_noalloc_scratch_bytes) and pa_abi_version.
+ *    pa_noalloc_scratch_bytes) and pa_abi_version; then the latent cache
+ *    (pa_latent_write, pa_latent_decode, pa_latent_prefill) and the block
+ *    tables on the device (pa_table_step, pa_table_compact).
  */
 #ifndef PA_H_
 #define PA_H_
@@ -103,6 +105,8 @@ typedef enum { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_FP8_E4M3 = 3 } pa_dtype;
                                       over the shared range */
 #define PA_DEVERR_STAGING 0x40u    /* pa_decode_fp8_rows / pa_decode_shared_prefix_fp8:
                                       the blocks to stage exceed staged_blocks */
+#define PA_DEVERR_POOL 0x80u       /* pa_table_step: the pool has too few free blocks */
+#define PA_DEVERR_TABLE 0x100u     /* pa_table_step: fork_src outside the rows */
 
 /*
  * pa_reshape_and_cache -- write this step's new K/V into their cache slots.
@@ -478,6 +482,205 @@ size_t pa_decode_shared_prefix_fp8_workspace_size(int num_seqs, int num_heads,
                                                   int max_blocks_per_seq,
                                                   int num_groups,
                                                   int staged_blocks);
+
+/*
+ * ---- Latent cache ---------------------------------------------------------
+ *
+ * A latent cache keeps one vector per token for all heads together:
+ * latent_dim values from which the keys and values of every head are linear
+ * maps, and rope_dim values that carry the position and enter the logits
+ * only.  It is paged like the K/V caches (same block tables, slots and error
+ * word): one pool
+ *     latent_cache  [num_blocks][block_size][latent_dim + rope_dim]
+ * Because the maps are linear, a head's query can be brought into the latent
+ * space once (absorbed form: the cache row itself is key and value) or the
+ * rows can be multiplied out to per-head keys and values (expanded form).
+ *
+ * Supported by pa_latent_write and pa_latent_decode: latent_dim in {256,
+ * 512}, rope_dim 64, block_size in {16, 32, 64}, PA_F16 and PA_BF16, any
+ * num_heads.
+ */
+
+/*
+ * pa_latent_write -- this step's new rows into their slots, the latent cache's
+ * pa_reshape_and_cache.
+ *
+ *   latent        [num_tokens] rows of latent_dim, latent_stride elements apart
+ *   rope          [num_tokens] rows of rope_dim, rope_stride elements apart
+ *                 (both may be slices of one projection's output rows; base
+ *                 pointers and row strides are multiples of 16 bytes)
+ *   slot_mapping  int64 [num_tokens]; negative = padding, skipped; no slot twice
+ * Byte-exact copy.  A slot past the pool is skipped and sets PA_DEVERR_SLOT.
+ */
+int pa_latent_write(const void *latent, const void *rope, void *latent_cache,
+                    const int64_t *slot_mapping, int num_tokens,
+                    int64_t latent_stride, int64_t rope_stride, int latent_dim,
+                    int rope_dim, int block_size, int num_blocks, int dtype,
+                    struct CUstream_st *stream);
+
+/*
+ * pa_latent_decode -- attention over the latent cache in the absorbed form.
+ * For context length L, rows t = 0..Q-1 of a sequence (Q = 1 for decode, a few
+ * for drafted tokens) and head h, with c_j the cache row of key j,
+ *     s_j = scale * q[t][h] . c_j            (latent_dim + rope_dim products)
+ *     out[t][h] = sum_j softmax(s)_j c_j[0 .. latent_dim)
+ *     lse[t][h] = ln sum_j exp(s_j)
+ * over the keys j <= L - Q + t.  A row that sees no key is written as zeros,
+ * its lse as -inf.  fp32 accumulation; the softmax weights enter the second
+ * product in the cache's type.
+ *
+ *   out               [num_q_tokens][num_heads][latent_dim], dtype
+ *   lse               float [num_q_tokens][num_heads], or NULL
+ *   q                 [num_q_tokens][num_heads][latent_dim + rope_dim]
+ *   block_tables, context_lens, query_start_loc, max_query_len,
+ *   max_context_len   as for pa_decode; rows of q, out and lse past the last
+ *                     sequence are left as they are
+ *   scale             finite and >= 0
+ *   workspace         >= pa_latent_decode_workspace_size(...) bytes, 16-byte
+ *                     aligned; calls whose kernels may overlap (other streams,
+ *                     two captured graphs) need one each
+ * Device checks: a context length outside [0, max_context_len]
+ * (PA_DEVERR_CONTEXT_LEN), more than max_query_len rows or row offsets out of
+ * range (PA_DEVERR_QUERY_LEN): the sequence's rows within the tensor are
+ * zeros.  A block id outside the pool (PA_DEVERR_BLOCK_ID) zeroes the rows of
+ * its sequence.
+ * Cache rows of keys that only some rows of a sequence see must be finite (a
+ * weight of 0 times infinity is NaN); slots past a sequence's context may hold
+ * anything.
+ */
+int pa_latent_decode(void *out, float *lse, const void *q,
+                     const void *latent_cache, const int32_t *block_tables,
+                     int max_blocks_per_seq, const int32_t *context_lens,
+                     const int32_t *query_start_loc, int num_seqs,
+                     int num_q_tokens, int max_query_len, int num_heads,
+                     int latent_dim, int rope_dim, int block_size,
+                     int num_blocks, float scale, int max_context_len,
+                     int dtype, void *workspace, size_t workspace_bytes,
+                     struct CUstream_st *stream);
+
+/* Workspace bytes pa_latent_decode needs (current device). */
+size_t pa_latent_decode_workspace_size(int num_seqs, int max_query_len,
+                                       int num_heads, int latent_dim);
+
+/*
+ * pa_latent_prefill -- attention of new tokens in the expanded form: per head
+ * a key of nope_dim values, the rope_dim values shared by all heads, and a
+ * value vector of v_dim.  For Q query rows and L keys of a sequence,
+ *     s_j = scale * (q[t][h][0..nope) . k_j[h] + q[t][h][nope..] . k_rope_j)
+ *     out[t][h] = sum_j softmax(s)_j v_j[h],  lse[t][h] = ln sum_j exp(s_j)
+ * over the keys j <= L - Q + t (causal != 0) or all L keys (causal == 0, for a
+ * cached prefix attended apart and merged by its lse).  A row that sees no key
+ * is written as zeros, its lse as -inf.
+ *
+ *   q        [num_q_tokens][num_heads][nope_dim + rope_dim], contiguous
+ *   k, v     [num_k_tokens] rows of num_heads heads; k_token_stride,
+ *            k_head_stride, v_token_stride, v_head_stride in elements (k and v
+ *            may be slices of one projection's output)
+ *   k_rope   [num_k_tokens] rows of rope_dim, k_rope_stride elements apart
+ *   out      [num_q_tokens][num_heads][v_dim], contiguous
+ *   lse      float [num_q_tokens][num_heads], or NULL
+ *   query_start_loc, context_start_loc  int32 [num_seqs + 1]: a sequence's
+ *            rows of q and its rows of k, k_rope and v
+ *   max_query_len  host bound of any sequence's Q
+ * Base pointers and strides are multiples of 16 bytes.  Supported: nope_dim =
+ * v_dim in {64, 128}, rope_dim 64, PA_F16 and PA_BF16, scale finite and >= 0.
+ * Device checks: offsets out of range or more than max_query_len rows set
+ * PA_DEVERR_QUERY_LEN (a sequence with more rows: zeros; offsets out of range:
+ * skipped).  Keys and values of tokens that only some rows of a sequence see
+ * must be finite.  Rows past the last sequence are left as they are.
+ */
+int pa_latent_prefill(void *out, float *lse, const void *q, const void *k,
+                      const void *k_rope, const void *v,
+                      int64_t k_token_stride, int64_t k_head_stride,
+                      int64_t k_rope_stride, int64_t v_token_stride,
+                      int64_t v_head_stride, const int32_t *query_start_loc,
+                      const int32_t *context_start_loc, int num_seqs,
+                      int num_q_tokens, int num_k_tokens, int max_query_len,
+                      int num_heads, int nope_dim, int rope_dim, int v_dim,
+                      float scale, int causal, int dtype,
+                      struct CUstream_st *stream);
+
+/*
+ * ---- Block tables on the device -------------------------------------------
+ *
+ * The host allocator's bookkeeping (tables, lengths, reference counts) held in
+ * device arrays, so that a captured decode loop grows, forks and releases its
+ * sequences without the host:
+ *     block_tables  int32 [num_seqs][max_blocks_per_seq]
+ *     context_lens  int32 [num_seqs]
+ *     ref_counts    int32 [num_blocks]; a block is free when its count is 0
+ * A row of length L holds its first ceil(L / block_size) entries; entries
+ * after them keep whatever they held.  Free blocks are taken lowest id first.
+ *
+ * pools: host array of num_pools device pointers, the caches that these tables
+ * page (K, V, latent, of any number of layers), each num_blocks blocks of
+ * pool_block_bytes[i] bytes (pointers and sizes multiples of 16); read during
+ * the call.  At most 1024 pools.
+ */
+
+/*
+ * pa_table_step -- one scheduling step of all rows, in this order:
+ *   1. rows with release[i] != 0 give up their blocks (length 0);
+ *   2. rows with fork_src[i] >= 0 give up theirs too and come to hold the
+ *      blocks and length that row fork_src[i] had before the step (so rows may
+ *      be permuted among themselves, and forked from rows released in the same
+ *      step);
+ *   3. rows grow by append[i] tokens, in row order.  A row whose last block is
+ *      partly filled and shared gets a block of its own for it first
+ *      (copy-on-write; of the rows that write into one block the last holder
+ *      keeps it).  When a row's blocks no longer fit the pool, it and all
+ *      later growing rows stay as they are and PA_DEVERR_POOL is set.
+ *
+ *   release, fork_src, append  int32 [num_seqs]; release and fork_src may be
+ *                   NULL.  append < 0, or more than the row's table holds:
+ *                   not grown, PA_DEVERR_CONTEXT_LEN.  fork_src >= num_seqs:
+ *                   not forked, PA_DEVERR_TABLE.
+ *   slot_mapping    int64 [max_new_tokens], written: the slots of the appended
+ *                   tokens, row after row; -1 for tokens of rows that did not
+ *                   grow and after the last one.  More tokens than
+ *                   max_new_tokens: the rest is dropped, PA_DEVERR_SLOT.
+ *   query_start_loc int32 [num_seqs + 1], written: offsets of each row's
+ *                   tokens in slot_mapping (counting every append[i] > 0)
+ *   copy_pairs      int64 [num_seqs][2], written: the row's (src, dst)
+ *                   copy-on-write copy, or (-1, -1); done in all pools here
+ *   workspace       >= pa_table_workspace_size(...) bytes
+ * Supported: 1 <= num_seqs <= 4096, max_blocks_per_seq * block_size <= 2^29.
+ * Lengths outside [0, max_blocks_per_seq *
+ * block_size] count as 0 (PA_DEVERR_CONTEXT_LEN); block ids outside the pool
+ * in a held entry are skipped (PA_DEVERR_BLOCK_ID).
+ */
+int pa_table_step(int32_t *block_tables, int max_blocks_per_seq,
+                  int32_t *context_lens, int32_t *ref_counts,
+                  const int32_t *release, const int32_t *fork_src,
+                  const int32_t *append, int num_seqs, int num_blocks,
+                  int block_size, int64_t *slot_mapping, int max_new_tokens,
+                  int32_t *query_start_loc, int64_t *copy_pairs,
+                  void *const *pools, const int64_t *pool_block_bytes,
+                  int num_pools, void *workspace, size_t workspace_bytes,
+                  struct CUstream_st *stream);
+
+/*
+ * pa_table_compact -- move the used blocks to the front of the pool.  With
+ * `live` used blocks, the k-th used block with an id >= live moves to the k-th
+ * free id < live; tables, counts and the blocks of all pools follow.
+ *   num_live     int32 [1], written: live
+ *   block_moves  int64 [max(1, num_blocks / 2)][2], written: (src, dst), the
+ *                rest (-1, -1)
+ * Blocks at ids >= live keep their bytes.  Held entries outside the pool stay
+ * and set PA_DEVERR_BLOCK_ID; lengths out of range count as 0
+ * (PA_DEVERR_CONTEXT_LEN).
+ */
+int pa_table_compact(int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *context_lens, int32_t *ref_counts,
+                     int num_seqs, int num_blocks, int block_size,
+                     int32_t *num_live, int64_t *block_moves,
+                     void *const *pools, const int64_t *pool_block_bytes,
+                     int num_pools, void *workspace, size_t workspace_bytes,
+                     struct CUstream_st *stream);
+
+/* Workspace bytes pa_table_step and pa_table_compact need. */
+size_t pa_table_workspace_size(int num_seqs, int max_blocks_per_seq,
+                               int num_blocks);
 
 /*
  * pa_get_device_error -- synchronise `stream`, then read and clear the

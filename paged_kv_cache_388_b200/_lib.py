@@ -59,6 +59,22 @@ _lib.pa_decode_shared_prefix_fp8.argtypes = [P, P, P, P, P, I, P, I, P, P, I, I,
                                              F, F, I, I, I, P, SZ, P]
 _lib.pa_decode_shared_prefix_fp8_workspace_size.restype = SZ
 _lib.pa_decode_shared_prefix_fp8_workspace_size.argtypes = [I, I, I, I, I, I, I, I, I]
+L = ctypes.c_int64
+_lib.pa_latent_write.restype = I
+_lib.pa_latent_write.argtypes = [P, P, P, P, I, L, L, I, I, I, I, I, P]
+_lib.pa_latent_decode.restype = I
+_lib.pa_latent_decode.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, F, I, I, P, SZ, P]
+_lib.pa_latent_decode_workspace_size.restype = SZ
+_lib.pa_latent_decode_workspace_size.argtypes = [I, I, I, I]
+_lib.pa_latent_prefill.restype = I
+_lib.pa_latent_prefill.argtypes = [P, P, P, P, P, P, L, L, L, L, L, P, P, I, I, I, I, I, I, I, I, F,
+                                   I, I, P]
+_lib.pa_table_step.restype = I
+_lib.pa_table_step.argtypes = [P, I, P, P, P, P, P, I, I, I, P, I, P, P, P, P, I, P, SZ, P]
+_lib.pa_table_compact.restype = I
+_lib.pa_table_compact.argtypes = [P, I, P, P, I, I, I, P, P, P, P, I, P, SZ, P]
+_lib.pa_table_workspace_size.restype = SZ
+_lib.pa_table_workspace_size.argtypes = [I, I, I]
 _lib.pa_noalloc_scratch_bytes.restype = SZ
 _lib.pa_noalloc_scratch_bytes.argtypes = []
 _lib.pa_get_device_error.restype = I
@@ -79,6 +95,8 @@ PA_DEVERR_QUERY_LEN = 0x8
 PA_DEVERR_TIMEOUT = 0x10
 PA_DEVERR_PREFIX = 0x20
 PA_DEVERR_STAGING = 0x40
+PA_DEVERR_POOL = 0x80
+PA_DEVERR_TABLE = 0x100
 
 
 class PAError(RuntimeError):
@@ -440,6 +458,216 @@ def pa_decode_shared_prefix_fp8(out, q, k_cache, v_cache, block_tables, context_
                                           int(staged_blocks), _DT[q.dtype], _ptr(workspace),
                                           ws_bytes, _stream(stream))
     _check(rc, "pa_decode_shared_prefix_fp8")
+
+
+def _dev_rows(t, name, dtype):
+    """A CUDA tensor on the current device whose last dimension is contiguous;
+    returns its element strides before it (a dimension of one row or head
+    counts as packed: torch leaves its stride arbitrary)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device} but the current device is "
+                         f"cuda:{torch.cuda.current_device()}; call under torch.cuda.device(...)")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    strides, packed = [], 1
+    for n, st in zip(reversed(t.shape), reversed(t.stride())):
+        strides.append(st if n > 1 else packed)
+        packed *= max(n, 1)
+    if strides[0] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if any(x % 8 for x in strides[1:]) or t.data_ptr() % 16:
+        raise ValueError(f"rows of {name} must start on 16-byte boundaries")
+    return strides[:0:-1]
+
+
+def _latent_shape(latent_cache):
+    """(num_blocks, block_size, row width) of a latent cache."""
+    _shape(latent_cache.dim() == 3,
+           "latent_cache must be [num_blocks, block_size, latent_dim + rope_dim]")
+    return tuple(latent_cache.shape)
+
+
+def pa_latent_write(latent, rope, latent_cache, slot_mapping, stream=None):
+    """latent [T, R] and rope [T, Dr] (rows may be strided slices); latent_cache
+    [NB, bs, R + Dr]; slot_mapping int64 [T], negative slots are skipped."""
+    nb, bs, w = _latent_shape(latent_cache)
+    _shape(latent.dim() == 2 and rope.dim() == 2 and latent.shape[0] == rope.shape[0],
+           "latent and rope must hold one row per token")
+    _shape(latent.shape[1] + rope.shape[1] == w,
+           f"latent and rope rows must add up to the cache's {w} values")
+    _shape(slot_mapping.dim() == 1 and slot_mapping.shape[0] == latent.shape[0],
+           "slot_mapping must hold one slot per token")
+    _dev(latent_cache, "latent_cache")
+    ls, = _dev_rows(latent, "latent", latent_cache.dtype)
+    rs, = _dev_rows(rope, "rope", latent_cache.dtype)
+    _dev(slot_mapping, "slot_mapping", torch.int64)
+    rc = _lib.pa_latent_write(_ptr(latent), _ptr(rope), _ptr(latent_cache), _ptr(slot_mapping),
+                              latent.shape[0], ls, rs, latent.shape[1], rope.shape[1], bs, nb,
+                              _DT.get(latent_cache.dtype, -1), _stream(stream))
+    _check(rc, "pa_latent_write")
+
+
+def pa_latent_decode_workspace_size(num_seqs, max_query_len, num_heads, latent_dim) -> int:
+    return int(_lib.pa_latent_decode_workspace_size(num_seqs, max_query_len, num_heads, latent_dim))
+
+
+def pa_latent_decode(out, lse, q, latent_cache, block_tables, context_lens, scale,
+                     query_start_loc=None, max_query_len=1, max_context_len=0, workspace=None,
+                     stream=None):
+    """out [Tq, H, R]; lse float32 [Tq, H] or None; q [Tq, H, R + Dr];
+    latent_cache [NB, bs, R + Dr]; block_tables int32 [S, mbps]; context_lens
+    int32 [S]; query_start_loc int32 [S + 1] or None; workspace: uint8 CUDA
+    tensor of >= pa_latent_decode_workspace_size(...) bytes."""
+    nb, bs, w = _latent_shape(latent_cache)
+    _shape(q.dim() == 3 and q.shape[2] == w, f"q must be [tokens, heads, {w}] to match the cache")
+    tq, h, _ = q.shape
+    _shape(out.dim() == 3 and tuple(out.shape[:2]) == (tq, h) and out.shape[2] < w,
+           "out must be [tokens, heads, latent_dim]")
+    r = out.shape[2]
+    _shape(lse is None or tuple(lse.shape) == (tq, h), "lse must be [tokens, heads]")
+    _shape(block_tables.dim() == 2, "block_tables must be [num_seqs, max_blocks_per_seq]")
+    s, mbps = block_tables.shape
+    _shape(context_lens.dim() == 1 and context_lens.shape[0] == s,
+           "block_tables and context_lens disagree on the number of sequences")
+    if query_start_loc is None:
+        _shape(tq == s, "without query_start_loc q must hold one row per sequence")
+    else:
+        _shape(query_start_loc.dim() == 1 and query_start_loc.shape[0] == s + 1,
+               "query_start_loc must have num_seqs + 1 entries")
+        _dev(query_start_loc, "query_start_loc", torch.int32)
+    _dev(q, "q")
+    _dev(out, "out", q.dtype)
+    _dev(latent_cache, "latent_cache", q.dtype)
+    _dev(block_tables, "block_tables", torch.int32)
+    _dev(context_lens, "context_lens", torch.int32)
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+    if workspace is not None:
+        _dev(workspace, "workspace")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _lib.pa_latent_decode(_ptr(out), _ptr(lse), _ptr(q), _ptr(latent_cache),
+                               _ptr(block_tables), mbps, _ptr(context_lens), _ptr(query_start_loc),
+                               s, tq, int(max_query_len), h, r, w - r, bs, nb, float(scale),
+                               int(max_context_len), _DT.get(q.dtype, -1), _ptr(workspace),
+                               ws_bytes, _stream(stream))
+    _check(rc, "pa_latent_decode")
+
+
+def pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_loc, scale,
+                      max_query_len, causal=True, stream=None):
+    """out [Tq, H, Dv]; lse float32 [Tq, H] or None; q [Tq, H, Dn + Dr]; k
+    [Tk, H, Dn], v [Tk, H, Dv] and k_rope [Tk, Dr] (tokens and heads may be
+    strided); query_start_loc and context_start_loc int32 [S + 1]."""
+    _shape(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and k_rope.dim() == 2,
+           "q, k and v must be [tokens, heads, dim], k_rope [tokens, dim]")
+    tq, h, dq = q.shape
+    tk, _, dn = k.shape
+    dr, dv = k_rope.shape[1], v.shape[2]
+    _shape(dn + dr == dq, "q rows must hold nope_dim + rope_dim values")
+    _shape(k.shape[1] == h and tuple(v.shape[:2]) == (tk, h) and k_rope.shape[0] == tk,
+           "k, v and k_rope must hold the same tokens, k and v q's heads")
+    _shape(tuple(out.shape) == (tq, h, dv), "out must be [tokens, heads, v_dim]")
+    _shape(lse is None or tuple(lse.shape) == (tq, h), "lse must be [tokens, heads]")
+    _shape(query_start_loc.dim() == 1 and query_start_loc.shape[0] >= 1 and
+           query_start_loc.shape == context_start_loc.shape,
+           "query_start_loc and context_start_loc must have num_seqs + 1 entries each")
+    _dev(q, "q")
+    _dev(out, "out", q.dtype)
+    ks, kh = _dev_rows(k, "k", q.dtype)
+    vs, vh = _dev_rows(v, "v", q.dtype)
+    krs, = _dev_rows(k_rope, "k_rope", q.dtype)
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+    _dev(query_start_loc, "query_start_loc", torch.int32)
+    _dev(context_start_loc, "context_start_loc", torch.int32)
+    rc = _lib.pa_latent_prefill(_ptr(out), _ptr(lse), _ptr(q), _ptr(k), _ptr(k_rope), _ptr(v),
+                                ks, kh, krs, vs, vh, _ptr(query_start_loc),
+                                _ptr(context_start_loc), query_start_loc.shape[0] - 1, tq, tk,
+                                int(max_query_len), h, dn, dr, dv, float(scale),
+                                1 if causal else 0, _DT.get(q.dtype, -1), _stream(stream))
+    _check(rc, "pa_latent_prefill")
+
+
+def _table_shapes(block_tables, context_lens, ref_counts):
+    _shape(block_tables.dim() == 2, "block_tables must be [num_seqs, max_blocks_per_seq]")
+    _shape(tuple(context_lens.shape) == (block_tables.shape[0],),
+           "block_tables and context_lens disagree on the number of sequences")
+    _shape(ref_counts.dim() == 1, "ref_counts must be [num_blocks]")
+    _dev(block_tables, "block_tables", torch.int32)
+    _dev(context_lens, "context_lens", torch.int32)
+    _dev(ref_counts, "ref_counts", torch.int32)
+    return (*block_tables.shape, ref_counts.shape[0])
+
+
+def _pool_args(pools, num_blocks):
+    """Host arrays of the pools' addresses and block bytes."""
+    n = len(pools)
+    ptrs, sizes = (P * max(n, 1))(), (L * max(n, 1))()
+    for i, t in enumerate(pools):
+        _dev(t, "pool")
+        _shape(t.dim() >= 1 and t.shape[0] == num_blocks,
+               f"a pool must hold {num_blocks} blocks, got {tuple(t.shape)}")
+        ptrs[i] = t.data_ptr()
+        sizes[i] = t.stride(0) * t.element_size() if num_blocks > 1 else t.numel() * t.element_size()
+    return ptrs, sizes, n
+
+
+def pa_table_workspace_size(num_seqs, max_blocks_per_seq, num_blocks) -> int:
+    return int(_lib.pa_table_workspace_size(num_seqs, max_blocks_per_seq, num_blocks))
+
+
+def pa_table_step(block_tables, context_lens, ref_counts, append, block_size, slot_mapping,
+                  query_start_loc, copy_pairs, release=None, fork_src=None, pools=(),
+                  workspace=None, stream=None):
+    """block_tables int32 [S, W], context_lens int32 [S] and ref_counts int32
+    [NB], updated in place; append, release, fork_src int32 [S]; slot_mapping
+    int64 [max_new_tokens], query_start_loc int32 [S + 1] and copy_pairs int64
+    [S, 2] are written; pools: CUDA tensors [NB, ...] whose blocks follow."""
+    s, w, nb = _table_shapes(block_tables, context_lens, ref_counts)
+    for name, t in (("append", append), ("release", release), ("fork_src", fork_src)):
+        if t is not None:
+            _shape(tuple(t.shape) == (s,), f"{name} must hold one entry per sequence")
+            _dev(t, name, torch.int32)
+    _shape(slot_mapping.dim() == 1, "slot_mapping must be [max_new_tokens]")
+    _shape(tuple(query_start_loc.shape) == (s + 1,),
+           "query_start_loc must have num_seqs + 1 entries")
+    _shape(tuple(copy_pairs.shape) == (s, 2), "copy_pairs must be [num_seqs, 2]")
+    _dev(slot_mapping, "slot_mapping", torch.int64)
+    _dev(query_start_loc, "query_start_loc", torch.int32)
+    _dev(copy_pairs, "copy_pairs", torch.int64)
+    ptrs, sizes, n = _pool_args(pools, nb)
+    if workspace is not None:
+        _dev(workspace, "workspace")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _lib.pa_table_step(_ptr(block_tables), w, _ptr(context_lens), _ptr(ref_counts),
+                            _ptr(release), _ptr(fork_src), _ptr(append), s, nb, int(block_size),
+                            _ptr(slot_mapping), slot_mapping.shape[0], _ptr(query_start_loc),
+                            _ptr(copy_pairs), ptrs, sizes, n, _ptr(workspace), ws_bytes,
+                            _stream(stream))
+    _check(rc, "pa_table_step")
+
+
+def pa_table_compact(block_tables, context_lens, ref_counts, block_size, num_live, block_moves,
+                     pools=(), workspace=None, stream=None):
+    """Move the used blocks to ids [0, live): block_tables, ref_counts and the
+    pools' blocks are updated in place; num_live int32 [1] and block_moves
+    int64 [max(1, NB // 2), 2] are written."""
+    s, w, nb = _table_shapes(block_tables, context_lens, ref_counts)
+    _shape(tuple(num_live.shape) == (1,), "num_live must be [1]")
+    _shape(tuple(block_moves.shape) == (max(1, nb // 2), 2),
+           "block_moves must be [max(1, num_blocks // 2), 2]")
+    _dev(num_live, "num_live", torch.int32)
+    _dev(block_moves, "block_moves", torch.int64)
+    ptrs, sizes, n = _pool_args(pools, nb)
+    if workspace is not None:
+        _dev(workspace, "workspace")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _lib.pa_table_compact(_ptr(block_tables), w, _ptr(context_lens), _ptr(ref_counts), s, nb,
+                               int(block_size), _ptr(num_live), _ptr(block_moves), ptrs, sizes, n,
+                               _ptr(workspace), ws_bytes, _stream(stream))
+    _check(rc, "pa_table_compact")
 
 
 def pa_noalloc_scratch_bytes() -> int:
