@@ -1,5 +1,6 @@
 // latent.cu -- the latent cache's entry points (argument checks) and the
 // scatter of new rows into their slots.
+#include <float.h>
 #include <math.h>
 
 #include "latent.h"
@@ -38,6 +39,10 @@ __global__ void __launch_bounds__(256) latent_write_kernel(
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool dtype16(int dtype) { return dtype == PA_F16 || dtype == PA_BF16; }
 bool scale_ok(float s) { return isfinite(s) && s >= 0.f; }
+
+// scale * log2(e); never 0, so that a masked -infinity stays one (a scale this
+// small leaves every finite logit at 0)
+float scale_log2(float scale) { return fmaxf(scale * 1.4426950408889634f, FLT_MIN); }
 
 // Checks shared by the entry points that take a latent cache.
 int latent_shape(int latent_dim, int rope_dim, int block_size, int dtype) {
@@ -143,7 +148,7 @@ int pa_latent_decode(void *out, float *lse, const void *q, const void *latent_ca
   a.num_blocks = num_blocks;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.max_context_len = max_context_len;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2(scale);
   a.ws = workspace;
   a.err = dev.err;
   const cudaError_t e = launch_latent_decode(a, dtype, dev.sm_count, (cudaStream_t)stream);
@@ -195,7 +200,7 @@ int pa_latent_prefill(void *out, float *lse, const void *q, const void *k, const
   a.num_heads = num_heads;
   a.nope_dim = nope_dim;
   a.causal = causal != 0;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2(scale);
   a.err = dev.err;
   const cudaError_t e = launch_latent_prefill(a, dtype, dev.sm_count, (cudaStream_t)stream);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

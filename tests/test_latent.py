@@ -335,6 +335,24 @@ def test_prefill_large_logits(lib):
     _check_prefill(lib, [300, 40], [600, 40], 2, 64, "f16", scale=0.0)
 
 
+def test_prefill_strides(lib):
+    """Heads before tokens, and token rows whose distance is no multiple of a head's."""
+    from paged_kv_cache_388_b200.latent import latent_prefill
+    g = torch.Generator().manual_seed(6)
+    n, heads = 150, 3
+    q = _randn(g, n, heads, 192).to(torch.bfloat16).cuda()
+    k, v = (_randn(g, n, heads, 128).to(torch.bfloat16).cuda() for _ in range(2))
+    kr = _randn(g, n, 64).to(torch.bfloat16).cuda()
+    sl = torch.tensor([0, n], dtype=torch.int32).cuda()
+    want = latent_prefill(q, k, kr, v, sl, sl, 0.07, max_query_len=n)
+    turned = k.transpose(0, 1).contiguous().transpose(0, 1)
+    wide = torch.zeros(n, heads * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    wide[:, :heads * 128] = v.reshape(n, -1)
+    padded = wide.as_strided((n, heads, 128), (heads * 128 + 8, 128, 1))
+    assert torch.equal(latent_prefill(q, turned, kr, padded, sl, sl, 0.07, max_query_len=n), want)
+    assert lib.pa_get_device_error() == 0
+
+
 def test_prefill_infinities_behind_the_last_key(lib):
     """Tokens of k, v and k_rope past a sequence's keys may hold anything."""
     from paged_kv_cache_388_b200.latent import latent_prefill
