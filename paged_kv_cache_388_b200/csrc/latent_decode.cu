@@ -1,101 +1,757 @@
-// latent_decode.cu -- attention over the latent cache in the absorbed form.
+// latent_decode.cu -- attention over the paged latent cache in the absorbed
+// form, on the 5th-generation tensor cores.
 //
-// The plain kernel: one CTA per (query row, head), its warps take keys in
-// turn with an online softmax each (running max m, sum l, weighted sum o in
-// registers) and are joined through shared memory.
+// Row r of a sequence is (token t, head h), r = t * H + h; its query q_r has R
+// latent and 64 rope values, as every cache row c_j does, and it sees the keys
+// j <= L-Q+t:
+//     s_rj = scale * q_r . c_j,  out_r = sum_j softmax(s_r)_j c_j[0..R)
+// The cache row is key and value at once, so a tile of keys is read once from
+// memory and used by two products.
+//
+// A CTA holds NR query rows (16, 32 or 64) in shared memory and streams tiles
+// of 64 keys.  What shapes the products is tensor memory: 128 rows of R = 512
+// fp32 sums would fill all of its 512 columns and leave none for S, so the
+// second product is turned round:
+//     S   [rows x keys] = Q C^T           M 64, N 64, K R+64
+//     O^T [values x rows] += C^T P^T      M 128 (R/128 times), N NR, K 64
+// O^T takes NR columns per 128 values (256 columns at NR 64, R 512) beside two
+// 64-column buffers of S.  A row of S lies in one thread (lanes 0-15 of each
+// warp's quarter hold 16 rows), so the softmax needs no exchange; P goes to
+// shared memory in the K-major layout that the B operand wants.  C is read
+// from shared memory as it lies: K-major for S, values-contiguous as the A
+// operand of O^T.  S(j+1) is issued before the product of P(j), so the
+// softmax runs under it.
+//
+// Keys arrive by TMA through the block table, one box a block: a 4-D view of
+// the cache splits rows into groups of 8 and each row into 64-value pieces, so
+// that a box lands as [8-key group][piece][8 keys][128 B] with one stride
+// between groups across the blocks of a tile.
+//
+// Work split: the tiles of all sequences form one line that is cut into equal
+// ranges, one per worker (ceil(rows / NR) CTAs, one per row tile, read the same
+// keys at the same time).  A sequence that lies in one range is written at
+// once; a cut one leaves a record (sums, maximum, total) per range, and the
+// merge kernel joins them in the order of the ranges.
+//
+// Bound: memory (each row of the cache once) up to about 64 rows a sequence,
+// beyond that the tensor cores.
 #include "latent.h"
 #include "pa_device.cuh"
+#include "tc_common.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kKeys = 64;                  // keys per tile
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8 between rescales
+constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kMaxSmem = 227 * 1024;
+constexpr int kBadSlots = 16;  // more than the items the producer can be ahead by
 
-template <typename T, int R>
-__global__ void __launch_bounds__(32 * kWarps) latent_decode_kernel(const LatentArgs a) {
-  constexpr int D = R + 64, PL = D / 32, PO = R / 32;
-  __shared__ float so[kWarps][R];
-  __shared__ float sm[kWarps], sl[kWarps];
-  __shared__ int bad;
-  const int H = a.num_heads, h = blockIdx.x % H;
-  const int t = (int)((blockIdx.x / H) % a.max_query_len), seq = (int)(blockIdx.x / H / a.max_query_len);
-  int q0 = seq, Q = 1;
+template <int R, int NR>
+struct Shape {
+  static constexpr int kD = R + 64;
+  static constexpr int kPieces = kD / 64;         // 64-value pieces of a row
+  static constexpr int kGroup = kPieces * 1024;   // bytes of 8 keys
+  static constexpr int kStage = kKeys / 8 * kGroup;
+  static constexpr int kQPiece = NR * 128;        // one piece of the Q rows
+  static constexpr int kQBytes = kPieces * kQPiece;
+  static constexpr int kPBytes = NR * 128;
+  static constexpr int kFixed = 1024 /* alignment */ + kPBytes + 1024 /* barriers, row state */;
+  // two Q buffers if two stages still fit
+  static constexpr int kQBufs = kFixed + 2 * kQBytes + 2 * kStage <= kMaxSmem ? 2 : 1;
+  static constexpr int kRoom = (kMaxSmem - kFixed - kQBufs * kQBytes) / kStage;
+  static constexpr int kStages = kRoom < 4 ? kRoom : 4;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffStage = kQBufs * kQBytes;
+  static constexpr int kOffP = kOffStage + kStages * kStage;
+  static constexpr int kOffBar = kOffP + kPBytes;
+  static constexpr int kSmem = kOffBar + 1024 + 1024;
+  static constexpr int kMTiles = R / 128;
+  static_assert(kStages >= 2, "two stages");
+  // the S product reads 64 rows from each Q piece: with fewer it runs into what
+  // follows (never past the allocation), and those rows of S are not used
+  static_assert(kOffQ + kQBufs * kQBytes + 64 * 128 <= kSmem, "Q reads stay inside");
+};
+
+enum {
+  kQFull = 0,            // [2]
+  kQEmpty = 2,           // [2]
+  kFull = 4,             // [4]
+  kEmpty = 8,            // [4]
+  kSFull = 12,           // [2]
+  kPFull = 14,
+  kPvDone = 15,
+  kOFree = 16,
+  kDone = 17,
+  kNumBars = 18
+};
+// words after the barriers
+constexpr int kWSlot = 2 * kNumBars;             // TMEM address
+constexpr int kWAbort = kWSlot + 1;
+constexpr int kWBad = kWAbort + 1;               // [kBadSlots]
+constexpr int kWStart = kWBad + kBadSlots;       // [2] first sequence, its first tile
+constexpr int kWScan = kWStart + 2;              // [8] block scan
+constexpr int kWRow = kWScan + 8;                // [2][64] rescale factors by tile parity / 1 over the sums
+static_assert((kWRow + 128) * 4 <= 1024, "row state");
+
+constexpr uint32_t kTmemO = 128;  // S: columns 0..127
+
+struct Seq {
+  int tiles, L, q0, Q;
+};
+
+// Sequence s as the kernels take it: no tiles if it has no keys, no rows, or
+// anything about it is out of range.
+__device__ __forceinline__ Seq seq_of(const LatentArgs &a, int s, unsigned int *err) {
+  Seq x;
+  x.q0 = s;
+  x.Q = 1;
+  x.L = a.context_lens[s];
   if (a.query_start_loc) {
-    q0 = a.query_start_loc[seq];
-    Q = a.query_start_loc[seq + 1] - q0;
-    if (q0 < 0 || Q < 0 || q0 > a.num_q_tokens - Q) {
-      raise_error(a.err, PA_DEVERR_QUERY_LEN);
-      return;
+    x.q0 = a.query_start_loc[s];
+    x.Q = a.query_start_loc[s + 1] - x.q0;
+  }
+  unsigned int bad = 0;
+  if (x.q0 < 0 || x.Q < 0 || x.q0 > a.num_q_tokens - x.Q) {
+    bad = PA_DEVERR_QUERY_LEN;
+    x.Q = 0;
+  } else if (x.Q > a.max_query_len) {
+    bad = PA_DEVERR_QUERY_LEN;
+  }
+  if (x.L < 0 || x.L > a.max_context_len) bad |= PA_DEVERR_CONTEXT_LEN;
+  if (bad) raise_error(err, bad);
+  x.tiles = bad || x.Q == 0 ? 0 : (x.L + kKeys - 1) / kKeys;
+  return x;
+}
+
+// A warp's view of consecutive sequences: 32 are read at once.
+struct Window {
+  int base;
+  Seq mine;
+  __device__ __forceinline__ void load(const LatentArgs &a, int s) {
+    base = s;
+    const int i = s + (int)(threadIdx.x & 31);
+    mine = Seq{0, 0, 0, 0};
+    if (i < a.num_seqs) mine = seq_of(a, i, nullptr);
+  }
+  __device__ __forceinline__ Seq get(const LatentArgs &a, int s) {
+    if (s >= base + 32) load(a, s);
+    Seq x;
+    x.tiles = __shfl_sync(0xffffffffu, mine.tiles, s - base);
+    x.L = __shfl_sync(0xffffffffu, mine.L, s - base);
+    x.q0 = __shfl_sync(0xffffffffu, mine.q0, s - base);
+    x.Q = __shfl_sync(0xffffffffu, mine.Q, s - base);
+    return x;
+  }
+};
+
+// The warp's walk over its worker's range: items (sequence, tiles [t0, t1)) in
+// which row tile `rt` has rows.
+struct Walk {
+  Window w;
+  int seq, off, left;
+  Seq x;
+  int t0, t1;
+  __device__ __forceinline__ void start(const LatentArgs &a, int s, int o, int n) {
+    seq = s - 1;
+    off = o;
+    left = n;
+    w.load(a, s);
+  }
+  __device__ __forceinline__ bool next(const LatentArgs &a, int first_row) {
+    while (left > 0 && ++seq < a.num_seqs) {
+      x = w.get(a, seq);
+      t0 = off;
+      off = 0;
+      const int take = min(left, x.tiles - t0);
+      if (take <= 0) continue;
+      t1 = t0 + take;
+      left -= take;
+      if (first_row < x.Q * a.num_heads) return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+
+// any thread's pred over the 128 softmax threads
+__device__ __forceinline__ bool vote_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
+
+template <typename T, int R, int NR, int BS>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap tmq,
+                         const __grid_constant__ CUtensorMap tmc, float *rec, float *rec_ml, int *pref,
+                         int workers, int row_tiles) {
+  using TT = TcType<T>;
+  using SH = Shape<R, NR>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SH::kOffBar);
+  volatile int *words = reinterpret_cast<volatile int *>(bars);
+  volatile float *rowf = reinterpret_cast<volatile float *>(words + kWRow);
+  volatile int *abort_flag = words + kWAbort;
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = a.num_heads;
+  const int worker = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles;
+  const int first_row = rt * NR;
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], i == kPFull || i == kOFree ? 4 : 1);
+    *abort_flag = 0;
+    for (int i = 0; i < kBadSlots; ++i) words[kWBad + i] = 0;
+    mbar_init_fence();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- the worker's range of tiles -----------------------------------------
+  volatile int *scan = words + kWScan;
+  unsigned int *err0 = blockIdx.x == 0 ? a.err : nullptr;
+  int sum = 0;
+  for (int s = tid; s < a.num_seqs; s += kThreads) sum += seq_of(a, s, err0).tiles;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane == 0) scan[warp] = sum;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += scan[w];
+  // no more workers than tiles, so that every worker between a cut sequence's
+  // first and last has a piece of it
+  workers = min(workers, total);
+  const int lo = worker < workers ? (int)((int64_t)total * worker / workers) : 0;
+  const int hi = worker < workers ? (int)((int64_t)total * (worker + 1) / workers) : 0;
+  if (lo >= hi && blockIdx.x != 0) return;  // CTA-uniform, before tensor memory is taken
+  int base = 0;
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+    const int s = s0 + tid;
+    const int n = s < a.num_seqs ? seq_of(a, s, nullptr).tiles : 0;
+    int x = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    __syncthreads();  // the previous use of scan[] is over
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int before = base, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      all += scan[w];
+    }
+    before += x - n;
+    if (n > 0 && before <= lo && lo < before + n) {
+      words[kWStart] = s;
+      words[kWStart + 1] = lo - before;
+    }
+    if (blockIdx.x == 0 && s < a.num_seqs) pref[s] = before;
+    base += all;
+    if (blockIdx.x != 0 && base > lo) break;  // CTA-uniform
+  }
+  if (blockIdx.x == 0 && tid == 0) pref[a.num_seqs] = total;
+  if (lo >= hi) return;
+
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     sbase + SH::kOffBar + 4 * kWSlot),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)words[kWSlot];
+
+  auto fail = [&](void) {
+    if (!*abort_flag) raise_error(a.err, PA_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  };
+  // a wait of a whole warp; after a failure nothing waits any more
+  auto warp_wait = [&](int bar, uint32_t parity) -> bool {
+    bool ok = !*abort_flag && mbar_wait(&bars[bar], parity);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && lane == 0) fail();
+    return ok;
+  };
+
+  Walk walk;
+  walk.start(a, words[kWStart], words[kWStart + 1], hi - lo);
+
+  if (warp == kProducerWarp) {
+    // ======================= producer =======================================
+    constexpr int kBpt = kKeys / BS;
+    uint32_t g = 0, item = 0;
+    bool ok = true;
+    while (ok && walk.next(a, first_row)) {
+      const int32_t *table = a.block_tables + (int64_t)walk.seq * a.max_blocks_per_seq;
+      const int nblk = (walk.x.L + BS - 1) / BS;
+      int grp = walk.t0 * kBpt;
+      int ids = grp + lane < nblk ? table[grp + lane] : 0;
+      int ids_next = grp + 32 + lane < nblk ? table[grp + 32 + lane] : 0;
+      const uint32_t qb = item % SH::kQBufs;
+      ok = warp_wait(kQEmpty + qb, ((item / SH::kQBufs) & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[kQFull + qb], SH::kQBytes);
+        for (int c = 0; c < SH::kPieces; ++c)
+          tma_load_2d(sbase + SH::kOffQ + qb * SH::kQBytes + c * SH::kQPiece, &tmq, c * 64,
+                      walk.x.q0 * H + first_row, &bars[kQFull + qb]);
+      }
+      for (int j = walk.t0; j < walk.t1; ++j, ++g) {
+        const uint32_t st = g % SH::kStages;
+        const int b0 = j * kBpt;
+        if (b0 >= grp + 32) {
+          grp += 32;
+          ids = ids_next;
+          ids_next = grp + 32 + lane < nblk ? table[grp + 32 + lane] : 0;
+        }
+        const int nb = min(kBpt, nblk - b0);
+        ok = warp_wait(kEmpty + st, ((g / SH::kStages) & 1) ^ 1);
+        if (!ok) break;
+        const int id = __shfl_sync(0xffffffffu, ids, (b0 - grp + lane) & 31);
+        const bool wrong = lane < nb && (id < 0 || id >= a.num_blocks);
+        if (wrong) {
+          raise_error(a.err, PA_DEVERR_BLOCK_ID);
+          words[kWBad + item % kBadSlots] = (int)item + 1;  // its rows are written as zeros
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&bars[kFull + st], nb * BS * SH::kD * 2);
+        __syncwarp();
+        if (lane < nb)  // a bad id is replaced by a valid block
+          tma_load_4d(sbase + SH::kOffStage + st * SH::kStage + lane * (BS / 8) * SH::kGroup, &tmc, 0, 0, 0,
+                      (wrong ? 0 : id) * (BS / 8), &bars[kFull + st]);
+        __syncwarp();
+      }
+      ++item;
+    }
+    // every copy has landed before the CTA can exit
+    if (lane == 0) {
+      bool landed = drain_ring(&bars[kFull], SH::kStages, g) && drain_ring(&bars[kQFull], SH::kQBufs, item);
+      if (!landed) fail();
+    }
+  } else if (warp == kMmaWarp) {
+    // ======================= MMA issue ======================================
+    constexpr uint32_t idesc_s = umma_idesc(TT::kFmt, 0, 0, 64, kKeys);
+    constexpr uint32_t idesc_pv = umma_idesc(TT::kFmt, 1, 0, 128, NR);
+    uint32_t g = 0, item = 0;
+    bool ok = true, pending = false, first = false;  // the previous tile's second product
+    auto issue_pv = [&]() -> bool {
+      const uint32_t p = g - 1, st = p % SH::kStages;
+      if (!warp_wait(kPFull, p & 1)) return false;
+      if (first && !warp_wait(kOFree, (item & 1) ^ 1)) return false;  // the item before has been read out
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t cst = sbase + SH::kOffStage + st * SH::kStage, pst = sbase + SH::kOffP;
+#pragma unroll
+        for (int mt = 0; mt < SH::kMTiles; ++mt)
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            umma(tmem + kTmemO + mt * NR, umma_desc(cst + mt * 2048 + ks * 2 * SH::kGroup, 1024, SH::kGroup),
+                 umma_desc(pst + ks * 32, 16, 1024), idesc_pv, (!first || ks > 0) ? 1u : 0u);
+        umma_commit(&bars[kEmpty + st]);
+        umma_commit(&bars[kPvDone]);
+      }
+      __syncwarp();
+      pending = false;
+      return true;
+    };
+    while (ok && walk.next(a, first_row)) {
+      const uint32_t qb = item % SH::kQBufs;
+      if (pending) {
+        --item;
+        ok = issue_pv();
+        ++item;
+      }
+      if (ok) ok = warp_wait(kQFull + qb, (item / SH::kQBufs) & 1);
+      for (int j = walk.t0; ok && j < walk.t1; ++j) {
+        const uint32_t st = g % SH::kStages;
+        ok = warp_wait(kFull + st, (g / SH::kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t cst = sbase + SH::kOffStage + st * SH::kStage;
+          const uint32_t qst = sbase + SH::kOffQ + qb * SH::kQBytes;
+#pragma unroll
+          for (int c = 0; c < SH::kPieces; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma(tmem + (g & 1) * kKeys, umma_desc(qst + c * SH::kQPiece + kk * 32, 16, 1024),
+                   umma_desc(cst + c * 1024 + kk * 32, 16, SH::kGroup), idesc_s, (c | kk) ? 1u : 0u);
+          umma_commit(&bars[kSFull + (g & 1)]);
+          if (j == walk.t1 - 1) umma_commit(&bars[kQEmpty + qb]);
+        }
+        __syncwarp();
+        if (pending) ok = issue_pv();
+        ++g;
+        pending = true;
+        first = j == walk.t0;
+      }
+      ++item;
+    }
+    if (ok && pending) {
+      --item;
+      ok = issue_pv();
+    }
+    // every product has finished before tensor memory is given back
+    if (lane == 0) {
+      umma_commit(&bars[kDone]);
+      if (!mbar_wait(&bars[kDone], 0)) fail();
+    }
+  } else {
+    // ======================= softmax warps ==================================
+    const int r = warp * 16 + lane;                // row of the tile: lanes 0-15
+    const bool has_rows = warp * 16 < NR;          // warp-uniform
+    const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16);
+    const float sl2 = a.scale_log2;
+    uint32_t g = 0, item = 0;
+    while (walk.next(a, first_row)) {
+      const Seq x = walk.x;
+      const int nrow = min(NR, x.Q * H - first_row);
+      const bool valid = lane < 16 && r < nrow;
+      const int limit = valid ? min(x.L - x.Q + (first_row + r) / H, x.L - 1) : -1;  // last key this row sees
+      const int limit_lo = min(x.L - x.Q + first_row / H, x.L - 1);                  // the tile's least
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = walk.t0; j < walk.t1; ++j, ++g) {
+        // after a failed wait the loop runs on without waiting, so that the
+        // four warps keep meeting at their barrier
+        ok = warp_wait(kSFull + (g & 1), (g >> 1) & 1) && ok;
+        tc_fence_after();
+        float alpha = 1.f;
+        bool need = false;
+        uint32_t w[32];
+        if (has_rows) {
+          uint32_t s[2][32];
+          tmem_ld32(ts + (g & 1) * kKeys, s[0]);
+          tmem_ld32(ts + (g & 1) * kKeys + 32, s[1]);
+          tmem_wait_ld();
+          const int kt = j * kKeys;
+          if (kt + kKeys - 1 > limit_lo) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              if (kt + i > limit) s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+          }
+          float mx2[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            mx2[c] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              mx2[c] = fmax3(mx2[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+          }
+          const float mx = fmaxf(mx2[0], mx2[1]) * sl2;
+          // lazy rescale: the reference moves when the tile's maximum exceeds it
+          // by more than 2^8 (first tile with a visible key: always)
+          need = valid && mx > m + kRescaleThreshold;
+          if (need) {
+            alpha = m == -INFINITY ? 0.f : fast_exp2(m - mx);
+            m = mx;
+            l *= alpha;
+          }
+          // the sum takes the unrounded weights, the product P rounded to 16 bits:
+          // half a step a weight, of the size of the result's own rounding
+          const float ref = m == -INFINITY ? 0.f : m;
+          const float2 sl2x2 = make_float2(sl2, sl2), negx2 = make_float2(-ref, -ref);
+          float2 psum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 v = make_float2(__uint_as_float(s[i >> 4][2 * (i & 15)]),
+                                         __uint_as_float(s[i >> 4][2 * (i & 15) + 1]));
+            const float2 e = __ffma2_rn(v, sl2x2, negx2);
+            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            psum = __fadd2_rn(psum, p);
+            w[i] = TT::pack(p.x, p.y);
+          }
+          l += psum.x + psum.y;
+        }
+        // P(j-1) and O are free once the second product of tile j-1 is done
+        const bool rest = j > walk.t0;
+        if (rest && has_rows && lane < 16 && r < NR) rowf[(g & 1) * 64 + r] = alpha;
+        const bool any = vote_any(need) && rest;
+        if (g > 0) ok = warp_wait(kPvDone, (g - 1) & 1) && ok;
+        if (any) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < SH::kMTiles * NR / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(ts + kTmemO + c * 16, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * rowf[(g & 1) * 64 + (c * 16 + i) % NR]);
+            tmem_st16(ts + kTmemO + c * 16, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        if (has_rows && lane < 16 && r < NR) {
+          const uint32_t dst = sbase + SH::kOffP + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            st_shared_v4(dst + ((c ^ (r & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        }
+        // slots past the last key: zero their values (P is 0 there, but 0 * NaN is not)
+        if ((j + 1) * kKeys > x.L) {
+          const uint32_t cst = sbase + SH::kOffStage + (g % SH::kStages) * SH::kStage;
+          const int z0 = x.L - j * kKeys;
+          for (int i = z0 * (R / 8) + tid; i < kKeys * (R / 8); i += 128) {
+            const int key = i / (R / 8), v = i % (R / 8);
+            st_shared_v4(cst + (key >> 3) * SH::kGroup + (v >> 3) * 1024 + (key & 7) * 128 + (v & 7) * 16, 0, 0,
+                         0, 0);
+          }
+        }
+        fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
+        tc_fence_before();         // reads of S and stores to O -> the MMA thread
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kPFull]);
+      }
+      // ---- epilogue ----
+      ok = warp_wait(kPvDone, (g - 1) & 1) && ok;
+      tc_fence_after();
+      const bool whole = walk.t0 == 0 && walk.t1 == x.tiles;
+      const bool bad = words[kWBad + item % kBadSlots] == (int)item + 1 || !ok;
+      const int64_t row0 = (int64_t)x.q0 * H + first_row;
+      const int64_t slot = ((int64_t)worker * 2 + (walk.t0 == 0 ? 1 : 0)) * row_tiles + rt;
+      if (valid) {
+        if (whole) {
+          rowf[r] = l > 0.f ? 1.f / l : (l != l ? l : 0.f);
+          if (a.lse)
+            a.lse[row0 + r] = bad ? -INFINITY : l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l != l ? l : -INFINITY);
+        } else {
+          rec_ml[(slot * NR + r) * 2] = m;
+          rec_ml[(slot * NR + r) * 2 + 1] = bad ? -1.f : l;  // a negative sum marks a bad sequence
+        }
+      }
+      named_sync(1, 128);
+      constexpr int kW = NR < 32 ? NR : 32;  // columns a load
+      for (int mt = 0; mt < SH::kMTiles; ++mt) {
+        const int dim = mt * 128 + warp * 32 + lane;
+#pragma unroll 1
+        for (int n0 = 0; n0 < NR; n0 += kW) {
+          if (n0 >= nrow) break;  // warp-uniform
+          uint32_t o[kW];
+          tmem_ld_cols(ts + kTmemO + mt * NR + n0, o);
+          tmem_wait_ld();
+          if (whole) {
+            // neighbouring lanes exchange, so that each stores two values of a row
+#pragma unroll
+            for (int i = 0; i < kW; i += 2) {
+              const float f0 = rowf[n0 + i], f1 = rowf[n0 + i + 1];
+              const float v0 = bad || f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
+              const float v1 = bad || f1 == 0.f ? 0.f : __uint_as_float(o[i + 1]) * f1;
+              const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
+              const int n = n0 + i + (lane & 1);
+              const uint32_t two = (lane & 1) ? TT::pack(other, v1) : TT::pack(v0, other);
+              if (n < nrow)
+                *reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + (row0 + n) * R + (dim & ~1)) = two;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kW; ++i)
+              if (n0 + i < nrow) rec[(slot * NR + n0 + i) * R + dim] = __uint_as_float(o[i]);
+          }
+        }
+      }
+      tc_fence_before();
+      named_sync(1, 128);  // rowf is rewritten by the next item
+      if (lane == 0) mbar_arrive(&bars[kOFree]);
+      ++item;
     }
   }
-  const int L = a.context_lens[seq];
-  const bool wrong = L < 0 || L > a.max_context_len || Q > a.max_query_len;
-  if (wrong && threadIdx.x == 0)
-    raise_error(a.err, Q > a.max_query_len ? PA_DEVERR_QUERY_LEN : PA_DEVERR_CONTEXT_LEN);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) bad = 0;
   __syncthreads();
-  for (int row = t; row < Q; row += a.max_query_len) {
-    const int64_t r = (int64_t)(q0 + row) * H + h;
-    const int n = wrong ? 0 : max(0, L - Q + row + 1);
-    float q[PL], o[PO], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < PL; ++i) q[i] = Elem<T>::to_f(static_cast<const T *>(a.q)[r * D + i * 32 + lane]);
-    for (int i = 0; i < PO; ++i) o[i] = 0.f;
-    for (int j = warp; j < n; j += kWarps) {
-      const int b = a.block_tables[(int64_t)seq * a.max_blocks_per_seq + j / a.block_size];
-      if (b < 0 || b >= a.num_blocks) {
-        raise_error(a.err, PA_DEVERR_BLOCK_ID);
-        bad = 1;
-        break;
-      }
-      const T *c = static_cast<const T *>(a.cache) + ((int64_t)b * a.block_size + j % a.block_size) * D;
-      float x[PL], s = 0.f;
-      for (int i = 0; i < PL; ++i) {
-        x[i] = Elem<T>::to_f(c[i * 32 + lane]);
-        s += q[i] * x[i];
-      }
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(s - mn);
-      l = l * f + p;
-      for (int i = 0; i < PO; ++i) o[i] = o[i] * f + p * x[i];
-      m = mn;
-    }
-    for (int i = 0; i < PO; ++i) so[warp][i * 32 + lane] = o[i];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// One CTA of R/4 threads per (sequence, row): joins the records of a sequence
+// that was cut, writes zeros where there is no key to see.
+constexpr int kMaxPieces = 512;
+template <typename T, int R>
+__global__ void __launch_bounds__(R / 4) latent_merge_kernel(const LatentArgs a, const float *rec,
+                                                             const float *rec_ml, const int *pref, int workers,
+                                                             int row_tiles, int NR) {
+  __shared__ float sw[kMaxPieces];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int per_seq = a.max_query_len * a.num_heads;
+  const int s = blockIdx.x / per_seq;
+  const Seq x = seq_of(a, s, nullptr);
+  const int rows = x.Q * a.num_heads, tid = threadIdx.x;
+  const int total = pref[a.num_seqs], p0 = pref[s];
+  workers = min(workers, total);
+  auto owner = [&](int t) { return (int)((((int64_t)t + 1) * workers - 1) / total); };
+  const int w0 = x.tiles ? owner(p0) : 0, w1 = x.tiles ? owner(p0 + x.tiles - 1) : 0;
+  if (x.tiles && w0 == w1) return;  // written by its worker
+  for (int row = blockIdx.x % per_seq; row < rows; row += per_seq) {
+    const int64_t orow = (int64_t)x.q0 * a.num_heads + row;
+    const int np = x.tiles ? w1 - w0 + 1 : 0;
+    const int rt = row / NR, r = row % NR;
+    // record of the i-th piece: the first starts the sequence, the others continue it
+    auto at = [&](int i) { return ((((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * row_tiles + rt) * NR + r); };
+    float M = -INFINITY;
+    bool bad = false;
+    for (int i = tid; i < np; i += R / 4) sw[i] = rec_ml[at(i) * 2];
     __syncthreads();
-    float M = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    for (int w = 0; w < kWarps; ++w) sum += sm[w] == -INFINITY ? 0.f : sl[w] * exp2f(sm[w] - M);
-    const bool none = M == -INFINITY || bad;
-    for (int d = threadIdx.x; d < R; d += 32 * kWarps) {
-      float x = 0.f;
-      for (int w = 0; w < kWarps; ++w)
-        if (sm[w] != -INFINITY) x += so[w][d] * exp2f(sm[w] - M);
-      static_cast<T *>(a.out)[r * R + d] = Elem<T>::from_f(none ? 0.f : x / sum);
+    for (int i = 0; i < np; ++i) M = fmaxf(M, sw[i]);
+    __syncthreads();
+    for (int i = tid; i < np; i += R / 4) sw[i] = sw[i] == -INFINITY ? 0.f : exp2f(sw[i] - M);
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+      const int64_t k = at(i);
+      const float lk = rec_ml[k * 2 + 1];
+      const float4 v = *reinterpret_cast<const float4 *>(rec + k * R + tid * 4);
+      const float f = sw[i];
+      bad = bad || lk < 0.f;
+      if (f == 0.f) continue;  // a piece without a visible key
+      l += f * lk;
+      o.x += f * v.x;
+      o.y += f * v.y;
+      o.z += f * v.z;
+      o.w += f * v.w;
     }
-    if (a.lse && threadIdx.x == 0)
-      a.lse[r] = none ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    const bool none = bad || l == 0.f;
+    const float inv = 1.f / l;
+    uint2 v = make_uint2(0, 0);
+    if (!none) {
+      v.x = TcType<T>::pack(o.x * inv, o.y * inv);
+      v.y = TcType<T>::pack(o.z * inv, o.w * inv);
+    }
+    *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + orow * R + tid * 4) = v;
+    if (a.lse && tid == 0) a.lse[orow] = none ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
     __syncthreads();
   }
 }
 
-template <typename T>
-cudaError_t launch_t(const LatentArgs &a, cudaStream_t s) {
-  const int64_t grid = (int64_t)a.num_seqs * a.max_query_len * a.num_heads;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  if (a.latent_dim == 512) latent_decode_kernel<T, 512><<<(unsigned)grid, 32 * kWarps, 0, s>>>(a);
-  else latent_decode_kernel<T, 256><<<(unsigned)grid, 32 * kWarps, 0, s>>>(a);
-  return cudaGetLastError();
+struct Plan {
+  int nr, row_tiles, workers;
+  size_t pref, ml, rec, total;  // workspace offsets
+};
+
+Plan plan_of(int num_seqs, int max_query_len, int num_heads, int latent_dim, int sm_count) {
+  Plan p;
+  const int64_t rows = (int64_t)max_query_len * num_heads;
+  // rows a CTA holds: fewer cost less in the second product (its N) and leave
+  // shared memory for the keys
+  p.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p.row_tiles = (int)((rows + p.nr - 1) / p.nr);
+  p.workers = sm_count / p.row_tiles;
+  if (p.workers < 1) p.workers = 1;
+  if (p.workers > kMaxPieces) p.workers = kMaxPieces;
+  const size_t recs = p.workers > 1 ? (size_t)p.workers * 2 * p.row_tiles * p.nr : 0;
+  p.pref = 0;
+  p.ml = ((size_t)(num_seqs + 1) * 4 + 255) / 256 * 256;
+  p.rec = p.ml + (recs * 8 + 255) / 256 * 256;
+  p.total = p.rec + recs * latent_dim * 4;
+  return p;
+}
+
+template <typename T, int R, int NR, int BS>
+cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
+  using SH = Shape<R, NR>;
+  auto fn = encode_fn_tc();
+  if (!fn) return cudaErrorNotSupported;
+  CUtensorMap tmq, tmc;
+  constexpr int D = R + 64;
+  CUresult r;
+  {
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.num_q_tokens * a.num_heads};
+    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)NR};
+    cuuint32_t estr[2] = {1, 1};
+    r = fn(&tmq, TcType<T>::kTma, 2, const_cast<void *>(a.q), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  if (r == CUDA_SUCCESS) {
+    // [8-key group][piece][8 keys][64 values], innermost first below
+    cuuint64_t dims[4] = {64, 8, (cuuint64_t)SH::kPieces, (cuuint64_t)a.num_blocks * (BS / 8)};
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16};
+    cuuint32_t box[4] = {64, 8, (cuuint32_t)SH::kPieces, (cuuint32_t)(BS / 8)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    r = fn(&tmc, TcType<T>::kTma, 4, const_cast<void *>(a.cache), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  if (r != CUDA_SUCCESS) {
+    debug_log("latent_decode: tensor map refused (CUresult %d)", (int)r);
+    return cudaErrorInvalidValue;
+  }
+  auto kern = latent_decode_kernel<T, R, NR, BS>;
+  cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(kern), SH::kSmem, true);
+  if (e != cudaSuccess) return e;
+  char *ws = static_cast<char *>(a.ws);
+  int *pref = reinterpret_cast<int *>(ws + p.pref);
+  float *ml = reinterpret_cast<float *>(ws + p.ml), *rec = reinterpret_cast<float *>(ws + p.rec);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3((unsigned)(p.workers * p.row_tiles));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = SH::kSmem;
+  e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmc, rec, ml, pref, p.workers, p.row_tiles);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)((int64_t)a.num_seqs * a.max_query_len * a.num_heads));
+  cfg.blockDim = dim3(R / 4);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<T, R>, a, (const float *)rec, (const float *)ml,
+                            (const int *)pref, p.workers, p.row_tiles, p.nr);
+}
+
+template <typename T, int R, int NR>
+cudaError_t launch_bs(const LatentArgs &a, const Plan &p, cudaStream_t s) {
+  if (a.block_size == 16) return launch_t<T, R, NR, 16>(a, p, s);
+  if (a.block_size == 32) return launch_t<T, R, NR, 32>(a, p, s);
+  return launch_t<T, R, NR, 64>(a, p, s);
+}
+
+template <typename T, int R>
+cudaError_t launch_nr(const LatentArgs &a, const Plan &p, cudaStream_t s) {
+  if (p.nr == 16) return launch_bs<T, R, 16>(a, p, s);
+  if (p.nr == 32) return launch_bs<T, R, 32>(a, p, s);
+  return launch_bs<T, R, 64>(a, p, s);
 }
 
 }  // namespace
 
-size_t latent_decode_ws(int, int, int, int, int) { return 0; }
+size_t latent_decode_ws(int num_seqs, int max_query_len, int num_heads, int latent_dim, int sm_count) {
+  return plan_of(num_seqs, max_query_len, num_heads, latent_dim, sm_count).total;
+}
 
-cudaError_t launch_latent_decode(const LatentArgs &a, int dtype, int, cudaStream_t stream) {
-  return dtype == PA_BF16 ? launch_t<__nv_bfloat16>(a, stream) : launch_t<__half>(a, stream);
+cudaError_t launch_latent_decode(const LatentArgs &a, int dtype, int sm_count, cudaStream_t stream) {
+  if ((int64_t)a.num_seqs * a.max_query_len * a.num_heads > 0x7fffffff) return cudaErrorInvalidValue;
+  const Plan p = plan_of(a.num_seqs, a.max_query_len, a.num_heads, a.latent_dim, sm_count);
+  if (dtype == PA_BF16)
+    return a.latent_dim == 512 ? launch_nr<__nv_bfloat16, 512>(a, p, stream)
+                               : launch_nr<__nv_bfloat16, 256>(a, p, stream);
+  return a.latent_dim == 512 ? launch_nr<__half, 512>(a, p, stream) : launch_nr<__half, 256>(a, p, stream);
 }
 
 }  // namespace pa
