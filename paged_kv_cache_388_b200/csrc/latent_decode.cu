@@ -44,8 +44,8 @@ namespace {
 
 constexpr int kKeys = 64;                  // keys per tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8 between rescales
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 192;
+constexpr int kProducerWarp = 4, kSWarp = 5, kPvWarp = 6;
+constexpr int kThreads = 224;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kBadSlots = 16;  // more than the items the producer can be ahead by
 
@@ -84,8 +84,9 @@ enum {
   kPFull = 14,
   kPvDone = 15,
   kOFree = 16,
-  kDone = 17,
-  kNumBars = 18
+  kSEmpty = 17,          // [2]
+  kDone = 19,            // [2]
+  kNumBars = 21
 };
 // words after the barriers
 constexpr int kWSlot = 2 * kNumBars;             // TMEM address
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_row = rt * NR;
 
   if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], i == kPFull || i == kOFree ? 4 : 1);
+    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], i == kPFull || i == kOFree || i == kSEmpty || i == kSEmpty + 1 ? 4 : 1);
     *abort_flag = 0;
     for (int i = 0; i < kBadSlots; ++i) words[kWBad + i] = 0;
     mbar_init_fence();
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && tid == 0) pref[a.num_seqs] = total;
   if (lo >= hi) return;
 
-  if (warp == kMmaWarp) {
+  if (warp == kSWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      sbase + SH::kOffBar + 4 * kWSlot),
                  "r"(512)
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // a wait of a whole warp; after a failure nothing waits any more
   auto warp_wait = [&](int bar, uint32_t parity) -> bool {
-    bool ok = !*abort_flag && mbar_wait(&bars[bar], parity);
+    bool ok = !*abort_flag && mbar_wait_spin(&bars[bar], parity);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) fail();
     return ok;
@@ -347,145 +348,173 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool landed = drain_ring(&bars[kFull], SH::kStages, g) && drain_ring(&bars[kQFull], SH::kQBufs, item);
       if (!landed) fail();
     }
-  } else if (warp == kMmaWarp) {
-    // ======================= MMA issue ======================================
-    constexpr uint32_t idesc_s = umma_idesc(TT::kFmt, 0, 0, 64, kKeys);
-    constexpr uint32_t idesc_pv = umma_idesc(TT::kFmt, 1, 0, 128, NR);
+  } else if (warp == kSWarp) {
+    // ======================= S = Q C^T ======================================
+    // The two products are issued by warps of their own: S(j+1) then runs under
+    // the softmax of tile j, and where its keys are still on the way the product
+    // of P(j) goes ahead and frees its stage.
+    constexpr uint32_t idesc = umma_idesc(TT::kFmt, 0, 0, 64, kKeys);
+    constexpr uint32_t kHiQ = umma_desc_hi(1024), kHiC = umma_desc_hi(SH::kGroup);
+    const uint32_t q_lo = umma_desc_lo(sbase + SH::kOffQ, 16), c_lo = umma_desc_lo(sbase + SH::kOffStage, 16);
     uint32_t g = 0, item = 0;
-    bool ok = true, pending = false, first = false;  // the previous tile's second product
-    auto issue_pv = [&]() -> bool {
-      const uint32_t p = g - 1, st = p % SH::kStages;
-      if (!warp_wait(kPFull, p & 1)) return false;
-      if (first && !warp_wait(kOFree, (item & 1) ^ 1)) return false;  // the item before has been read out
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t cst = sbase + SH::kOffStage + st * SH::kStage, pst = sbase + SH::kOffP;
-#pragma unroll
-        for (int mt = 0; mt < SH::kMTiles; ++mt)
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
-            umma(tmem + kTmemO + mt * NR, umma_desc(cst + mt * 2048 + ks * 2 * SH::kGroup, 1024, SH::kGroup),
-                 umma_desc(pst + ks * 32, 16, 1024), idesc_pv, (!first || ks > 0) ? 1u : 0u);
-        umma_commit(&bars[kEmpty + st]);
-        umma_commit(&bars[kPvDone]);
-      }
-      __syncwarp();
-      pending = false;
-      return true;
-    };
-    while (ok && walk.next(a, first_row)) {
+    bool ok = true;
+    for (; ok && walk.next(a, first_row); ++item) {
       const uint32_t qb = item % SH::kQBufs;
-      if (pending) {
-        --item;
-        ok = issue_pv();
-        ++item;
-      }
-      if (ok) ok = warp_wait(kQFull + qb, (item / SH::kQBufs) & 1);
-      for (int j = walk.t0; ok && j < walk.t1; ++j) {
+      ok = warp_wait(kQFull + qb, (item / SH::kQBufs) & 1);
+      for (int j = walk.t0; ok && j < walk.t1; ++j, ++g) {
         const uint32_t st = g % SH::kStages;
-        ok = warp_wait(kFull + st, (g / SH::kStages) & 1);
+        ok = warp_wait(kFull + st, (g / SH::kStages) & 1) && warp_wait(kSEmpty + (g & 1), ((g >> 1) & 1) ^ 1);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t cst = sbase + SH::kOffStage + st * SH::kStage;
-          const uint32_t qst = sbase + SH::kOffQ + qb * SH::kQBytes;
+        if (elect_one()) {
+          const uint32_t b_lo = c_lo + st * (SH::kStage >> 4), a_lo = q_lo + qb * (SH::kQBytes >> 4);
+          const uint32_t d = tmem + (g & 1) * kKeys;
 #pragma unroll
           for (int c = 0; c < SH::kPieces; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma(tmem + (g & 1) * kKeys, umma_desc(qst + c * SH::kQPiece + kk * 32, 16, 1024),
-                   umma_desc(cst + c * 1024 + kk * 32, 16, SH::kGroup), idesc_s, (c | kk) ? 1u : 0u);
+              umma_lo(d, a_lo + ((c * SH::kQPiece + kk * 32) >> 4), kHiQ, b_lo + ((c * 1024 + kk * 32) >> 4), kHiC,
+                      idesc, (c | kk) ? 1u : 0u);
           umma_commit(&bars[kSFull + (g & 1)]);
           if (j == walk.t1 - 1) umma_commit(&bars[kQEmpty + qb]);
         }
         __syncwarp();
-        if (pending) ok = issue_pv();
-        ++g;
-        pending = true;
-        first = j == walk.t0;
       }
-      ++item;
-    }
-    if (ok && pending) {
-      --item;
-      ok = issue_pv();
     }
     // every product has finished before tensor memory is given back
-    if (lane == 0) {
+    if (elect_one()) {
       umma_commit(&bars[kDone]);
       if (!mbar_wait(&bars[kDone], 0)) fail();
     }
+  } else if (warp == kPvWarp) {
+    // ======================= O^T += C^T P^T =================================
+    constexpr uint32_t idesc = umma_idesc(TT::kFmt, 1, 0, 128, NR);
+    constexpr uint32_t kHiP = umma_desc_hi(1024), kHiC = umma_desc_hi(SH::kGroup);
+    const uint32_t p_lo = umma_desc_lo(sbase + SH::kOffP, 16), v_lo = umma_desc_lo(sbase + SH::kOffStage, 1024);
+    uint32_t g = 0, item = 0;
+    bool ok = true;
+    for (; ok && walk.next(a, first_row); ++item) {
+      ok = warp_wait(kOFree, (item & 1) ^ 1);  // the sums of the item before have been read out
+      for (int j = walk.t0; ok && j < walk.t1; ++j, ++g) {
+        const uint32_t st = g % SH::kStages;
+        ok = warp_wait(kPFull, g & 1);  // P is written; the keys landed before S was computed
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t a_lo = v_lo + st * (SH::kStage >> 4);
+          const uint32_t keep = j == walk.t0 ? 0u : 1u;
+#pragma unroll
+          for (int mt = 0; mt < SH::kMTiles; ++mt)
+#pragma unroll
+            for (int ks = 0; ks < kKeys / 16; ++ks)
+              umma_lo(tmem + kTmemO + mt * NR, a_lo + ((mt * 2048 + ks * 2 * SH::kGroup) >> 4), kHiC,
+                      p_lo + ((ks * 32) >> 4), kHiP, idesc, ks > 0 ? 1u : keep);
+          umma_commit(&bars[kEmpty + st]);
+          umma_commit(&bars[kPvDone]);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) {
+      umma_commit(&bars[kDone + 1]);
+      if (!mbar_wait(&bars[kDone + 1], 0)) fail();
+    }
   } else {
     // ======================= softmax warps ==================================
-    const int r = warp * 16 + lane;                // row of the tile: lanes 0-15
-    const bool has_rows = warp * 16 < NR;          // warp-uniform
+    // A warp's quarter holds 16 rows; the thread has two of them, 8 apart, and 16
+    // of their 64 keys: two neighbours in every group of 8.
+    const int r0 = warp * 16 + (lane >> 2);
+    const bool has_rows = warp * 16 < NR;  // warp-uniform
     const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16);
     const float sl2 = a.scale_log2;
+    // where this lane's 16-byte row of P goes in a store of four 8x8 pieces
+    const int pr = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+    const uint32_t pdst = sbase + SH::kOffP + (pr >> 3) * 1024 + (pr & 7) * 128;
     uint32_t g = 0, item = 0;
     while (walk.next(a, first_row)) {
       const Seq x = walk.x;
       const int nrow = min(NR, x.Q * H - first_row);
-      const bool valid = lane < 16 && r < nrow;
-      const int limit = valid ? min(x.L - x.Q + (first_row + r) / H, x.L - 1) : -1;  // last key this row sees
-      const int limit_lo = min(x.L - x.Q + first_row / H, x.L - 1);                  // the tile's least
-      float m = -INFINITY, l = 0.f;
+      bool valid[2];
+      int limit[2];  // last key the row sees
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        valid[i] = r0 + 8 * i < nrow;
+        limit[i] = valid[i] ? min(x.L - x.Q + (first_row + r0 + 8 * i) / H, x.L - 1) : -1;
+      }
+      const int limit_lo = min(x.L - x.Q + first_row / H, x.L - 1);  // the tile's least
       bool ok = true;
       for (int j = walk.t0; j < walk.t1; ++j, ++g) {
         // after a failed wait the loop runs on without waiting, so that the
         // four warps keep meeting at their barrier
         ok = warp_wait(kSFull + (g & 1), (g >> 1) & 1) && ok;
         tc_fence_after();
-        float alpha = 1.f;
+        float alpha[2] = {1.f, 1.f};
         bool need = false;
-        uint32_t w[32];
+        uint32_t s[32], w[16];
         if (has_rows) {
-          uint32_t s[2][32];
-          tmem_ld32(ts + (g & 1) * kKeys, s[0]);
-          tmem_ld32(ts + (g & 1) * kKeys + 32, s[1]);
+          tmem_ld16x64(ts + (g & 1) * kKeys, s);
           tmem_wait_ld();
+        }
+        tc_fence_before();  // S has been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kSEmpty + (g & 1)]);
+        if (has_rows) {
           const int kt = j * kKeys;
           if (kt + kKeys - 1 > limit_lo) {
+            const int k0 = kt + 2 * (lane & 3);
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i)
-              if (kt + i > limit) s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 32; ++i)
+              if (k0 + 8 * (i >> 2) + (i & 1) > limit[(i >> 1) & 1]) s[i] = __float_as_uint(-INFINITY);
           }
-          float mx2[2];
+          // the two rows side by side, so that their chains overlap
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            mx2[c] = -INFINITY;
+          for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              mx2[c] = fmax3(mx2[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-          }
-          const float mx = fmaxf(mx2[0], mx2[1]) * sl2;
-          // lazy rescale: the reference moves when the tile's maximum exceeds it
-          // by more than 2^8 (first tile with a visible key: always)
-          need = valid && mx > m + kRescaleThreshold;
-          if (need) {
-            alpha = m == -INFINITY ? 0.f : fast_exp2(m - mx);
-            m = mx;
-            l *= alpha;
-          }
-          // the sum takes the unrounded weights, the product P rounded to 16 bits:
-          // half a step a weight, of the size of the result's own rounding
-          const float ref = m == -INFINITY ? 0.f : m;
-          const float2 sl2x2 = make_float2(sl2, sl2), negx2 = make_float2(-ref, -ref);
-          float2 psum = make_float2(0.f, 0.f);
+            for (int i = 0; i < 2; ++i)
+              mx[i] = fmax3(mx[i], __uint_as_float(s[4 * k + 2 * i]), __uint_as_float(s[4 * k + 2 * i + 1]));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 v = make_float2(__uint_as_float(s[i >> 4][2 * (i & 15)]),
-                                         __uint_as_float(s[i >> 4][2 * (i & 15) + 1]));
-            const float2 e = __ffma2_rn(v, sl2x2, negx2);
-            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            psum = __fadd2_rn(psum, p);
-            w[i] = TT::pack(p.x, p.y);
+          for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
+          float2 psum[2], negx2[2];
+          const float2 sl2x2 = make_float2(sl2, sl2);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // lazy rescale: the reference moves when the tile's maximum exceeds
+            // it by more than 2^8 (first tile with a visible key: always)
+            const float top = mx[i] * sl2;
+            const bool up = valid[i] && top > m[i] + kRescaleThreshold;
+            need = need || up;
+            alpha[i] = up ? (m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - top)) : 1.f;
+            m[i] = up ? top : m[i];
+            const float ref = m[i] == -INFINITY ? 0.f : m[i];
+            negx2[i] = make_float2(-ref, -ref);
+            psum[i] = make_float2(0.f, 0.f);
           }
-          l += psum.x + psum.y;
+          // the sum takes the unrounded weights, the product P rounded to 16
+          // bits: half a step a weight, of the size of the result's own rounding
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 v = make_float2(__uint_as_float(s[4 * k + 2 * i]), __uint_as_float(s[4 * k + 2 * i + 1]));
+              const float2 e = __ffma2_rn(v, sl2x2, negx2[i]);
+              const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+              psum[i] = __fadd2_rn(psum[i], p);
+              w[2 * k + i] = TT::pack(p.x, p.y);
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) l[i] = l[i] * alpha[i] + (psum[i].x + psum[i].y);
         }
-        // P(j-1) and O are free once the second product of tile j-1 is done
         const bool rest = j > walk.t0;
-        if (rest && has_rows && lane < 16 && r < NR) rowf[(g & 1) * 64 + r] = alpha;
+        if (rest && has_rows && (lane & 3) == 0) {
+          rowf[(g & 1) * 64 + r0] = alpha[0];
+          rowf[(g & 1) * 64 + r0 + 8] = alpha[1];
+        }
         const bool any = vote_any(need) && rest;
+        // P(j-1) and O are free once the second product of tile j-1 is done
         if (g > 0) ok = warp_wait(kPvDone, (g - 1) & 1) && ok;
         if (any) {
           tc_fence_after();
@@ -500,13 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(ts + kTmemO + c * 16, o);
           }
           tmem_wait_st();
-          tc_fence_before();
         }
-        if (has_rows && lane < 16 && r < NR) {
-          const uint32_t dst = sbase + SH::kOffP + (r >> 3) * 1024 + (r & 7) * 128;
+        if (has_rows) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_shared_v4(dst + ((c ^ (r & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          for (int k = 0; k < 8; k += 2)  // pieces: rows 0-7 and 8-15 of keys 8k.., then of keys 8(k+1)..
+            stsm_x4(pdst + (((k + (lane >> 4)) ^ (pr & 7)) << 4), w[2 * k], w[2 * k + 1], w[2 * k + 2], w[2 * k + 3]);
         }
         // slots past the last key: zero their values (P is 0 there, but 0 * NaN is not)
         if ((j + 1) * kKeys > x.L) {
@@ -519,25 +546,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
-        tc_fence_before();         // reads of S and stores to O -> the MMA thread
+        tc_fence_before();         // stores to O -> the issuing thread
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kPFull]);
       }
       // ---- epilogue ----
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      }
       ok = warp_wait(kPvDone, (g - 1) & 1) && ok;
       tc_fence_after();
       const bool whole = walk.t0 == 0 && walk.t1 == x.tiles;
       const bool bad = words[kWBad + item % kBadSlots] == (int)item + 1 || !ok;
       const int64_t row0 = (int64_t)x.q0 * H + first_row;
       const int64_t slot = ((int64_t)worker * 2 + (walk.t0 == 0 ? 1 : 0)) * row_tiles + rt;
-      if (valid) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 8 * i;
+        if (!valid[i] || (lane & 3)) continue;
         if (whole) {
-          rowf[r] = l > 0.f ? 1.f / l : (l != l ? l : 0.f);
+          rowf[r] = l[i] > 0.f ? 1.f / l[i] : (l[i] != l[i] ? l[i] : 0.f);
           if (a.lse)
-            a.lse[row0 + r] = bad ? -INFINITY : l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l != l ? l : -INFINITY);
+            a.lse[row0 + r] = bad ? -INFINITY : l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f
+                                              : (l[i] != l[i] ? l[i] : -INFINITY);
         } else {
-          rec_ml[(slot * NR + r) * 2] = m;
-          rec_ml[(slot * NR + r) * 2 + 1] = bad ? -1.f : l;  // a negative sum marks a bad sequence
+          rec_ml[(slot * NR + r) * 2] = m[i];
+          rec_ml[(slot * NR + r) * 2 + 1] = bad ? -1.f : l[i];  // a negative sum marks a bad sequence
         }
       }
       named_sync(1, 128);
@@ -577,72 +613,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kSWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
   }
 }
 
-// One CTA of R/4 threads per (sequence, row): joins the records of a sequence
-// that was cut, writes zeros where there is no key to see.
+// Joins the records of the sequences that were cut, writes zeros where there
+// is no key to see.  One CTA per (sequence, rows_per_cta rows): 8 rows, a warp
+// each, when there are rows enough to fill the machine, else one row whose
+// pieces the 8 warps share and join through shared memory (one long sequence
+// is cut into as many pieces as there are workers).
 constexpr int kMaxPieces = 512;
+constexpr int kMergeWarps = 8;
 template <typename T, int R>
-__global__ void __launch_bounds__(R / 4) latent_merge_kernel(const LatentArgs a, const float *rec,
-                                                             const float *rec_ml, const int *pref, int workers,
-                                                             int row_tiles, int NR) {
-  __shared__ float sw[kMaxPieces];
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    latent_merge_kernel(const LatentArgs a, const float *rec, const float *rec_ml, const int *pref, int workers,
+                        int row_tiles, int NR, int rows_per_cta) {
+  constexpr int V = R / 128;  // float4 a lane: values lane * 4 + 128 v
+  __shared__ float4 so[kMergeWarps][R / 4];
+  __shared__ float sl[kMergeWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int per_seq = a.max_query_len * a.num_heads;
+  const int per_seq = (a.max_query_len * a.num_heads + rows_per_cta - 1) / rows_per_cta;
   const int s = blockIdx.x / per_seq;
   const Seq x = seq_of(a, s, nullptr);
-  const int rows = x.Q * a.num_heads, tid = threadIdx.x;
+  const int rows = x.Q * a.num_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = pref[a.num_seqs], p0 = pref[s];
   workers = min(workers, total);
   auto owner = [&](int t) { return (int)((((int64_t)t + 1) * workers - 1) / total); };
   const int w0 = x.tiles ? owner(p0) : 0, w1 = x.tiles ? owner(p0 + x.tiles - 1) : 0;
   if (x.tiles && w0 == w1) return;  // written by its worker
-  for (int row = blockIdx.x % per_seq; row < rows; row += per_seq) {
-    const int64_t orow = (int64_t)x.q0 * a.num_heads + row;
-    const int np = x.tiles ? w1 - w0 + 1 : 0;
+  const int np = x.tiles ? w1 - w0 + 1 : 0;
+  const bool shared_row = rows_per_cta == 1;
+  const int step = shared_row ? kMergeWarps : 1;
+  for (int base = (int)(blockIdx.x % per_seq) * rows_per_cta; base < rows; base += per_seq * rows_per_cta) {
+    const int row = base + (shared_row ? 0 : warp);
+    if (row >= rows) break;  // a whole warp, and only where no barrier follows
     const int rt = row / NR, r = row % NR;
     // record of the i-th piece: the first starts the sequence, the others continue it
     auto at = [&](int i) { return ((((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * row_tiles + rt) * NR + r); };
     float M = -INFINITY;
-    bool bad = false;
-    for (int i = tid; i < np; i += R / 4) sw[i] = rec_ml[at(i) * 2];
-    __syncthreads();
-    for (int i = 0; i < np; ++i) M = fmaxf(M, sw[i]);
-    __syncthreads();
-    for (int i = tid; i < np; i += R / 4) sw[i] = sw[i] == -INFINITY ? 0.f : exp2f(sw[i] - M);
-    __syncthreads();
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = lane; i < np; i += 32) M = fmaxf(M, rec_ml[at(i) * 2]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float4 o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
+    bool bad = false;
 #pragma unroll 4
-    for (int i = 0; i < np; ++i) {
+    for (int i = shared_row ? warp : 0; i < np; i += step) {
       const int64_t k = at(i);
-      const float lk = rec_ml[k * 2 + 1];
-      const float4 v = *reinterpret_cast<const float4 *>(rec + k * R + tid * 4);
-      const float f = sw[i];
-      bad = bad || lk < 0.f;
-      if (f == 0.f) continue;  // a piece without a visible key
-      l += f * lk;
-      o.x += f * v.x;
-      o.y += f * v.y;
-      o.z += f * v.z;
-      o.w += f * v.w;
+      const float2 ml = *reinterpret_cast<const float2 *>(rec_ml + k * 2);
+      float4 p[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[v] = __ldcs(reinterpret_cast<const float4 *>(rec + k * R + v * 128 + lane * 4));
+      bad = bad || ml.y < 0.f;
+      // a piece without a visible key has no sums (a NaN total is not one)
+      const bool empty = ml.x == -INFINITY && ml.y <= 0.f;
+      const float f = empty ? 0.f : exp2f(ml.x - M);
+      l += empty ? 0.f : f * ml.y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        o[v].x += empty ? 0.f : f * p[v].x;
+        o[v].y += empty ? 0.f : f * p[v].y;
+        o[v].z += empty ? 0.f : f * p[v].z;
+        o[v].w += empty ? 0.f : f * p[v].w;
+      }
     }
+    if (shared_row) {  // one row a CTA: the barriers are uniform
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) so[warp][v * 32 + lane] = o[v];
+      if (lane == 0) sl[warp] = bad ? -INFINITY : l;
+      __syncthreads();
+      if (warp) continue;
+      for (int w = 1; w < kMergeWarps; ++w) {
+        bad = bad || sl[w] == -INFINITY;
+        l += sl[w];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float4 y = so[w][v * 32 + lane];
+          o[v].x += y.x;
+          o[v].y += y.y;
+          o[v].z += y.z;
+          o[v].w += y.w;
+        }
+      }
+    }
+    const int64_t orow = (int64_t)x.q0 * a.num_heads + row;
     const bool none = bad || l == 0.f;
     const float inv = 1.f / l;
-    uint2 v = make_uint2(0, 0);
-    if (!none) {
-      v.x = TcType<T>::pack(o.x * inv, o.y * inv);
-      v.y = TcType<T>::pack(o.z * inv, o.w * inv);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      uint2 y = make_uint2(0, 0);
+      if (!none) {
+        y.x = TcType<T>::pack(o[v].x * inv, o[v].y * inv);
+        y.y = TcType<T>::pack(o[v].z * inv, o[v].w * inv);
+      }
+      *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + orow * R + v * 128 + lane * 4) = y;
     }
-    *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + orow * R + tid * 4) = v;
-    if (a.lse && tid == 0) a.lse[orow] = none ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
-    __syncthreads();
+    if (a.lse && lane == 0) a.lse[orow] = none ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -718,11 +791,13 @@ cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
   cfg.dynamicSmemBytes = SH::kSmem;
   e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmc, rec, ml, pref, p.workers, p.row_tiles);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)((int64_t)a.num_seqs * a.max_query_len * a.num_heads));
-  cfg.blockDim = dim3(R / 4);
+  const int64_t rows = (int64_t)a.max_query_len * a.num_heads;
+  const int rows_per_cta = a.num_seqs * rows >= 4096 ? kMergeWarps : 1;
+  cfg.gridDim = dim3((unsigned)(a.num_seqs * ((rows + rows_per_cta - 1) / rows_per_cta)));
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, latent_merge_kernel<T, R>, a, (const float *)rec, (const float *)ml,
-                            (const int *)pref, p.workers, p.row_tiles, p.nr);
+                            (const int *)pref, p.workers, p.row_tiles, p.nr, rows_per_cta);
 }
 
 template <typename T, int R, int NR>
