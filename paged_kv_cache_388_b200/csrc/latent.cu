@@ -126,9 +126,8 @@ int pa_latent_decode(void *out, float *lse, const void *q, const void *latent_ca
   if (max_query_len > num_q_tokens) max_query_len = num_q_tokens;
   const int cap = max_blocks_per_seq * block_size;
   if (max_context_len <= 0 || max_context_len > cap) max_context_len = cap;
-  // the kernels count tiles of all sequences in 32 bits
-  if ((int64_t)num_seqs * ((max_context_len + 63) / 64) > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-  if ((int64_t)num_seqs * max_query_len * num_heads > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+  if (!latent_decode_fits(num_seqs, max_query_len, num_heads, latent_dim, max_context_len))
+    return PA_ERR_UNSUPPORTED;
   DevInfo dev;
   if (device_info(&dev) != cudaSuccess) return PA_ERR_CUDA;
   const size_t need = latent_decode_ws(num_seqs, max_query_len, num_heads, latent_dim, dev.sm_count);

@@ -21,6 +21,8 @@ struct LatentArgs {
   unsigned int *err;
 };
 size_t latent_decode_ws(int num_seqs, int max_query_len, int num_heads, int latent_dim, int sm_count);
+// Whether the kernels' 32-bit counts hold the batch.
+bool latent_decode_fits(int num_seqs, int max_query_len, int num_heads, int latent_dim, int max_context_len);
 cudaError_t launch_latent_decode(const LatentArgs &a, int dtype, int sm_count, cudaStream_t stream);
 
 // Expanded form over ragged contiguous keys and values (latent_prefill.cu).

@@ -35,6 +35,8 @@
 //
 // Bound: memory (each row of the cache once) up to about 64 rows a sequence,
 // beyond that the tensor cores.
+#include <limits.h>
+
 #include "latent.h"
 #include "pa_device.cuh"
 #include "tc_common.cuh"
@@ -42,60 +44,68 @@
 namespace pa {
 namespace {
 
-constexpr int kKeys = 64;                  // keys per tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8 between rescales
 constexpr int kProducerWarp = 4, kSWarp = 5, kPvWarp = 6;
 constexpr int kThreads = 224;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kBadSlots = 16;  // more than the items the producer can be ahead by
+constexpr int kMaxStages = 6;
+// What an item costs beside its tiles (its queries, its epilogue), in tiles:
+// with it the ranges of a batch of short and long sequences end together.
+constexpr int kItemTiles = 2;
 
-template <int R, int NR>
+// KT keys a tile
+template <int R, int NR, int KT>
 struct Shape {
   static constexpr int kD = R + 64;
   static constexpr int kPieces = kD / 64;         // 64-value pieces of a row
   static constexpr int kGroup = kPieces * 1024;   // bytes of 8 keys
-  static constexpr int kStage = kKeys / 8 * kGroup;
+  static constexpr int kStage = KT / 8 * kGroup;
   static constexpr int kQPiece = NR * 128;        // one piece of the Q rows
   static constexpr int kQBytes = kPieces * kQPiece;
-  static constexpr int kPBytes = NR * 128;
-  static constexpr int kFixed = 1024 /* alignment */ + kPBytes + 1024 /* barriers, row state */;
-  // two Q buffers if two stages still fit
-  static constexpr int kQBufs = kFixed + 2 * kQBytes + 2 * kStage <= kMaxSmem ? 2 : 1;
+  // two buffers of P: 128-byte rows of 64 keys each, or of the two halves of one
+  static constexpr int kPBytes = (KT == 64 ? 2 : 1) * NR * 128;
+  static constexpr int kPNext = KT == 64 ? NR * 128 : 64;
+  static constexpr int kFixed = 1024 /* alignment */ + kPBytes + 2048 /* barriers, row state */;
+  // two Q buffers where enough stages still fit
+  static constexpr int kWant = KT == 64 ? 3 : 4;
+  static constexpr int kQBufs = kFixed + 2 * kQBytes + kWant * kStage <= kMaxSmem ? 2 : 1;
   static constexpr int kRoom = (kMaxSmem - kFixed - kQBufs * kQBytes) / kStage;
-  static constexpr int kStages = kRoom < 4 ? kRoom : 4;
+  static constexpr int kStages = kRoom < kMaxStages ? kRoom : kMaxStages;
   static constexpr int kOffQ = 0;
   static constexpr int kOffStage = kQBufs * kQBytes;
   static constexpr int kOffP = kOffStage + kStages * kStage;
   static constexpr int kOffBar = kOffP + kPBytes;
-  static constexpr int kSmem = kOffBar + 1024 + 1024;
+  static constexpr int kSmem = kOffBar + 2048 + 1024;
   static constexpr int kMTiles = R / 128;
-  static_assert(kStages >= 2, "two stages");
+  static_assert(kStages >= 2 && kSmem <= kMaxSmem, "two stages");
   // the S product reads 64 rows from each Q piece: with fewer it runs into what
   // follows (never past the allocation), and those rows of S are not used
   static_assert(kOffQ + kQBufs * kQBytes + 64 * 128 <= kSmem, "Q reads stay inside");
 };
 
 enum {
-  kQFull = 0,            // [2]
-  kQEmpty = 2,           // [2]
-  kFull = 4,             // [4]
-  kEmpty = 8,            // [4]
-  kSFull = 12,           // [2]
-  kPFull = 14,
-  kPvDone = 15,
-  kOFree = 16,
-  kSEmpty = 17,          // [2]
-  kDone = 19,            // [2]
-  kNumBars = 21
+  kQFull = 0,                      // [2]
+  kQEmpty = 2,                     // [2]
+  kFull = 4,                       // [kMaxStages]
+  kEmpty = kFull + kMaxStages,     // [kMaxStages]
+  kSFull = kEmpty + kMaxStages,    // [2]
+  kSEmpty = kSFull + 2,            // [2]
+  kPFull = kSEmpty + 2,            // [2]
+  kPvDone = kPFull + 2,            // [2]
+  kOFree = kPvDone + 2,
+  kDone = kOFree + 1,              // [2]
+  kNumBars = kDone + 2
 };
 // words after the barriers
 constexpr int kWSlot = 2 * kNumBars;             // TMEM address
 constexpr int kWAbort = kWSlot + 1;
 constexpr int kWBad = kWAbort + 1;               // [kBadSlots]
-constexpr int kWStart = kWBad + kBadSlots;       // [2] first sequence, its first tile
+constexpr int kWStart = kWBad + kBadSlots;       // [2] first sequence, its first unit
 constexpr int kWScan = kWStart + 2;              // [8] block scan
-constexpr int kWRow = kWScan + 8;                // [2][64] rescale factors by tile parity / 1 over the sums
-static_assert((kWRow + 128) * 4 <= 1024, "row state");
+constexpr int kWAlpha = kWScan + 8;              // [2][64] rescale factors, by tile parity
+constexpr int kWInv = kWAlpha + 128;             // [2][64] 1 over the sums, by item parity
+static_assert((kWInv + 128) * 4 <= 2048, "row state");
 
 constexpr uint32_t kTmemO = 128;  // S: columns 0..127
 
@@ -103,9 +113,24 @@ struct Seq {
   int tiles, L, q0, Q;
 };
 
+// How the work is laid out in a line of units.  Lockstep: a sequence has
+// kItemTiles + tiles units and each worker is `lanes` CTAs, one per row tile,
+// that read the same keys at the same time (one of them from memory).  Flat
+// (lanes 1): a sequence has that many units per row tile it really has, and a
+// worker is one CTA; for batches whose sequences differ in rows.
+struct Line {
+  int workers, lanes, flat, nr, kt;
+  __device__ __forceinline__ int row_tiles(const Seq &x, int heads) const {
+    return flat ? (x.Q * heads + nr - 1) / nr : 1;
+  }
+  __device__ __forceinline__ int units(const Seq &x, int heads) const {
+    return x.tiles ? (x.tiles + kItemTiles) * row_tiles(x, heads) : 0;
+  }
+};
+
 // Sequence s as the kernels take it: no tiles if it has no keys, no rows, or
 // anything about it is out of range.
-__device__ __forceinline__ Seq seq_of(const LatentArgs &a, int s, unsigned int *err) {
+__device__ __forceinline__ Seq seq_of(const LatentArgs &a, const Line &ln, int s, unsigned int *err) {
   Seq x;
   x.q0 = s;
   x.Q = 1;
@@ -123,61 +148,62 @@ __device__ __forceinline__ Seq seq_of(const LatentArgs &a, int s, unsigned int *
   }
   if (x.L < 0 || x.L > a.max_context_len) bad |= PA_DEVERR_CONTEXT_LEN;
   if (bad) raise_error(err, bad);
-  x.tiles = bad || x.Q == 0 ? 0 : (x.L + kKeys - 1) / kKeys;
+  x.tiles = bad || x.Q == 0 ? 0 : (x.L + ln.kt - 1) / ln.kt;
   return x;
 }
 
-// A warp's view of consecutive sequences: 32 are read at once.
-struct Window {
+// A warp's walk over its worker's range: items (sequence, row tile, tiles [t0,
+// t1)).  32 sequences are read at once, one a lane.
+struct Walk {
+  const LatentArgs &a;
+  const Line &ln;
   int base;
   Seq mine;
-  __device__ __forceinline__ void load(const LatentArgs &a, int s) {
+  int seq, off, left, lane_rt;
+  // the item
+  Seq x;
+  int first_row, t0, t1;
+  __device__ __forceinline__ Walk(const LatentArgs &args, const Line &line, int s, int o, int n, int rt)
+      : a(args), ln(line), seq(s), off(o), left(n), lane_rt(rt) {
+    load(s);
+    t0 = t1 = first_row = 0;
+    x = Seq{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ void load(int s) {
     base = s;
     const int i = s + (int)(threadIdx.x & 31);
     mine = Seq{0, 0, 0, 0};
-    if (i < a.num_seqs) mine = seq_of(a, i, nullptr);
+    if (i < a.num_seqs) mine = seq_of(a, ln, i, nullptr);
   }
-  __device__ __forceinline__ Seq get(const LatentArgs &a, int s) {
-    if (s >= base + 32) load(a, s);
-    Seq x;
-    x.tiles = __shfl_sync(0xffffffffu, mine.tiles, s - base);
-    x.L = __shfl_sync(0xffffffffu, mine.L, s - base);
-    x.q0 = __shfl_sync(0xffffffffu, mine.q0, s - base);
-    x.Q = __shfl_sync(0xffffffffu, mine.Q, s - base);
-    return x;
-  }
-};
-
-// The warp's walk over its worker's range: items (sequence, tiles [t0, t1)) in
-// which row tile `rt` has rows.
-struct Walk {
-  Window w;
-  int seq, off, left;
-  Seq x;
-  int t0, t1;
-  __device__ __forceinline__ void start(const LatentArgs &a, int s, int o, int n) {
-    seq = s - 1;
-    off = o;
-    left = n;
-    w.load(a, s);
-  }
-  __device__ __forceinline__ bool next(const LatentArgs &a, int first_row) {
-    while (left > 0 && ++seq < a.num_seqs) {
-      x = w.get(a, seq);
-      t0 = off;
-      off = 0;
-      const int take = min(left, x.tiles - t0);
-      if (take <= 0) continue;
-      t1 = t0 + take;
+  __device__ __forceinline__ bool next() {
+    while (left > 0 && seq < a.num_seqs) {
+      if (seq >= base + 32) load(seq);
+      x.tiles = __shfl_sync(0xffffffffu, mine.tiles, seq - base);
+      x.L = __shfl_sync(0xffffffffu, mine.L, seq - base);
+      x.q0 = __shfl_sync(0xffffffffu, mine.q0, seq - base);
+      x.Q = __shfl_sync(0xffffffffu, mine.Q, seq - base);
+      if (off >= ln.units(x, a.num_heads)) {
+        ++seq;
+        off = 0;
+        continue;
+      }
+      const int per = x.tiles + kItemTiles;
+      const int rt = ln.flat ? off / per : 0;
+      const int at = off - rt * per;
+      const int take = min(left, per - at);
+      off += take;
       left -= take;
-      if (first_row < x.Q * a.num_heads) return true;
+      t0 = max(0, at - kItemTiles);
+      t1 = max(0, at + take - kItemTiles);
+      first_row = (rt + lane_rt) * ln.nr;
+      if (t1 > t0 && first_row < x.Q * a.num_heads) return true;
     }
     return false;
   }
 };
 
-__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+__device__ __forceinline__ void tmem_ld_s(uint32_t addr, uint32_t (&r)[32]) { tmem_ld16x64(addr, r); }
+__device__ __forceinline__ void tmem_ld_s(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16x32(addr, r); }
 
 // any thread's pred over the 128 softmax threads
 __device__ __forceinline__ bool vote_any(bool pred) {
@@ -191,28 +217,28 @@ __device__ __forceinline__ bool vote_any(bool pred) {
   return r != 0;
 }
 
-template <typename T, int R, int NR, int BS>
+template <typename T, int R, int NR, int KT, int BS>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap tmq,
                          const __grid_constant__ CUtensorMap tmc, float *rec, float *rec_ml, int *pref,
-                         int workers, int row_tiles) {
+                         const Line line) {
   using TT = TcType<T>;
-  using SH = Shape<R, NR>;
+  using SH = Shape<R, NR, KT>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + SH::kOffBar);
   volatile int *words = reinterpret_cast<volatile int *>(bars);
-  volatile float *rowf = reinterpret_cast<volatile float *>(words + kWRow);
+  volatile float *row_alpha = reinterpret_cast<volatile float *>(words + kWAlpha);
+  volatile float *row_inv = reinterpret_cast<volatile float *>(words + kWInv);
   volatile int *abort_flag = words + kWAbort;
   const uint32_t sbase = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = a.num_heads;
-  const int worker = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles;
-  const int first_row = rt * NR;
+  const int worker = blockIdx.x / line.lanes, rt = blockIdx.x % line.lanes;
 
   if (tid == 0) {
-    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], i == kPFull || i == kOFree || i == kSEmpty || i == kSEmpty + 1 ? 4 : 1);
+    for (int i = 0; i < kNumBars; ++i) mbar_init(&bars[i], (i >= kSEmpty && i < kPvDone) || i == kOFree ? 4 : 1);
     *abort_flag = 0;
     for (int i = 0; i < kBadSlots; ++i) words[kWBad + i] = 0;
     mbar_init_fence();
@@ -220,11 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- the worker's range of tiles -----------------------------------------
+  // ---- the worker's range of units -----------------------------------------
   volatile int *scan = words + kWScan;
   unsigned int *err0 = blockIdx.x == 0 ? a.err : nullptr;
   int sum = 0;
-  for (int s = tid; s < a.num_seqs; s += kThreads) sum += seq_of(a, s, err0).tiles;
+  for (int s = tid; s < a.num_seqs; s += kThreads) sum += line.units(seq_of(a, line, s, err0), H);
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0) scan[warp] = sum;
@@ -232,16 +258,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   int total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) total += scan[w];
-  // no more workers than tiles, so that every worker between a cut sequence's
+  // no more workers than units, so that every worker between a cut sequence's
   // first and last has a piece of it
-  workers = min(workers, total);
+  const int workers = min(line.workers, total);
   const int lo = worker < workers ? (int)((int64_t)total * worker / workers) : 0;
   const int hi = worker < workers ? (int)((int64_t)total * (worker + 1) / workers) : 0;
   if (lo >= hi && blockIdx.x != 0) return;  // CTA-uniform, before tensor memory is taken
   int base = 0;
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     const int s = s0 + tid;
-    const int n = s < a.num_seqs ? seq_of(a, s, nullptr).tiles : 0;
+    const int n = s < a.num_seqs ? line.units(seq_of(a, line, s, nullptr), H) : 0;
     int x = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -285,26 +311,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!*abort_flag) raise_error(a.err, PA_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
-  // a wait of a whole warp; after a failure nothing waits any more
+  // a wait of a whole warp; the clock, whose read takes longer than a poll, and
+  // the flag of a failure elsewhere are looked at on every 64th
   auto warp_wait = [&](int bar, uint32_t parity) -> bool {
-    bool ok = !*abort_flag && mbar_wait_spin(&bars[bar], parity);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok && lane == 0) fail();
+    bool ok = false;
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!ok && !*abort_flag && globaltimer_ns() - t0 <= kWaitLimitNs)
+        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) fail();
+    }
     return ok;
   };
 
-  Walk walk;
-  walk.start(a, words[kWStart], words[kWStart + 1], hi - lo);
+  Walk walk(a, line, words[kWStart], words[kWStart + 1], hi - lo, rt);
 
   if (warp == kProducerWarp) {
     // ======================= producer =======================================
-    constexpr int kBpt = kKeys / BS;
+    constexpr int kBox = BS < KT ? BS : KT;  // keys a box
+    constexpr int kBpt = KT / kBox;
     uint32_t g = 0, item = 0;
     bool ok = true;
-    while (ok && walk.next(a, first_row)) {
+    while (ok && walk.next()) {
       const int32_t *table = a.block_tables + (int64_t)walk.seq * a.max_blocks_per_seq;
       const int nblk = (walk.x.L + BS - 1) / BS;
-      int grp = walk.t0 * kBpt;
+      // 32 ids at a time, the next 32 on their way
+      int grp = walk.t0 * KT / BS;
       int ids = grp + lane < nblk ? table[grp + lane] : 0;
       int ids_next = grp + 32 + lane < nblk ? table[grp + 32 + lane] : 0;
       const uint32_t qb = item % SH::kQBufs;
@@ -314,31 +348,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&bars[kQFull + qb], SH::kQBytes);
         for (int c = 0; c < SH::kPieces; ++c)
           tma_load_2d(sbase + SH::kOffQ + qb * SH::kQBytes + c * SH::kQPiece, &tmq, c * 64,
-                      walk.x.q0 * H + first_row, &bars[kQFull + qb]);
+                      walk.x.q0 * H + walk.first_row, &bars[kQFull + qb]);
       }
       for (int j = walk.t0; j < walk.t1; ++j, ++g) {
         const uint32_t st = g % SH::kStages;
-        const int b0 = j * kBpt;
-        if (b0 >= grp + 32) {
+        const int key = j * KT + lane * kBox, blk = key / BS;  // this lane's box
+        if (j * KT / BS >= grp + 32) {
           grp += 32;
           ids = ids_next;
           ids_next = grp + 32 + lane < nblk ? table[grp + 32 + lane] : 0;
         }
-        const int nb = min(kBpt, nblk - b0);
+        const int nb = min(kBpt, (walk.x.L - j * KT + kBox - 1) / kBox);
         ok = warp_wait(kEmpty + st, ((g / SH::kStages) & 1) ^ 1);
         if (!ok) break;
-        const int id = __shfl_sync(0xffffffffu, ids, (b0 - grp + lane) & 31);
+        const int id = __shfl_sync(0xffffffffu, ids, (blk - grp) & 31);
         const bool wrong = lane < nb && (id < 0 || id >= a.num_blocks);
         if (wrong) {
           raise_error(a.err, PA_DEVERR_BLOCK_ID);
           words[kWBad + item % kBadSlots] = (int)item + 1;  // its rows are written as zeros
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&bars[kFull + st], nb * BS * SH::kD * 2);
+        if (lane == 0) mbar_arrive_expect_tx(&bars[kFull + st], nb * kBox * SH::kD * 2);
         __syncwarp();
         if (lane < nb)  // a bad id is replaced by a valid block
-          tma_load_4d(sbase + SH::kOffStage + st * SH::kStage + lane * (BS / 8) * SH::kGroup, &tmc, 0, 0, 0,
-                      (wrong ? 0 : id) * (BS / 8), &bars[kFull + st]);
+          tma_load_4d(sbase + SH::kOffStage + st * SH::kStage + lane * (kBox / 8) * SH::kGroup, &tmc, 0, 0, 0,
+                      (wrong ? 0 : id) * (BS / 8) + (key % BS) / 8, &bars[kFull + st]);
         __syncwarp();
       }
       ++item;
@@ -353,12 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The two products are issued by warps of their own: S(j+1) then runs under
     // the softmax of tile j, and where its keys are still on the way the product
     // of P(j) goes ahead and frees its stage.
-    constexpr uint32_t idesc = umma_idesc(TT::kFmt, 0, 0, 64, kKeys);
+    constexpr uint32_t idesc = umma_idesc(TT::kFmt, 0, 0, 64, KT);
     constexpr uint32_t kHiQ = umma_desc_hi(1024), kHiC = umma_desc_hi(SH::kGroup);
     const uint32_t q_lo = umma_desc_lo(sbase + SH::kOffQ, 16), c_lo = umma_desc_lo(sbase + SH::kOffStage, 16);
     uint32_t g = 0, item = 0;
     bool ok = true;
-    for (; ok && walk.next(a, first_row); ++item) {
+    for (; ok && walk.next(); ++item) {
       const uint32_t qb = item % SH::kQBufs;
       ok = warp_wait(kQFull + qb, (item / SH::kQBufs) & 1);
       for (int j = walk.t0; ok && j < walk.t1; ++j, ++g) {
@@ -368,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (elect_one()) {
           const uint32_t b_lo = c_lo + st * (SH::kStage >> 4), a_lo = q_lo + qb * (SH::kQBytes >> 4);
-          const uint32_t d = tmem + (g & 1) * kKeys;
+          const uint32_t d = tmem + (g & 1) * KT;
 #pragma unroll
           for (int c = 0; c < SH::kPieces; ++c)
 #pragma unroll
@@ -393,24 +426,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_lo = umma_desc_lo(sbase + SH::kOffP, 16), v_lo = umma_desc_lo(sbase + SH::kOffStage, 1024);
     uint32_t g = 0, item = 0;
     bool ok = true;
-    for (; ok && walk.next(a, first_row); ++item) {
+    for (; ok && walk.next(); ++item) {
       ok = warp_wait(kOFree, (item & 1) ^ 1);  // the sums of the item before have been read out
       for (int j = walk.t0; ok && j < walk.t1; ++j, ++g) {
         const uint32_t st = g % SH::kStages;
-        ok = warp_wait(kPFull, g & 1);  // P is written; the keys landed before S was computed
+        ok = warp_wait(kPFull + (g & 1), (g >> 1) & 1);  // P is written; the keys landed before S was computed
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t a_lo = v_lo + st * (SH::kStage >> 4);
+          const uint32_t a_lo = v_lo + st * (SH::kStage >> 4), b_lo = p_lo + (g & 1) * (SH::kPNext >> 4);
           const uint32_t keep = j == walk.t0 ? 0u : 1u;
 #pragma unroll
           for (int mt = 0; mt < SH::kMTiles; ++mt)
 #pragma unroll
-            for (int ks = 0; ks < kKeys / 16; ++ks)
+            for (int ks = 0; ks < KT / 16; ++ks)
               umma_lo(tmem + kTmemO + mt * NR, a_lo + ((mt * 2048 + ks * 2 * SH::kGroup) >> 4), kHiC,
-                      p_lo + ((ks * 32) >> 4), kHiP, idesc, ks > 0 ? 1u : keep);
+                      b_lo + ((ks * 32) >> 4), kHiP, idesc, ks > 0 ? 1u : keep);
           umma_commit(&bars[kEmpty + st]);
-          umma_commit(&bars[kPvDone]);
+          umma_commit(&bars[kPvDone + (g & 1)]);
         }
         __syncwarp();
       }
@@ -421,18 +454,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ======================= softmax warps ==================================
-    // A warp's quarter holds 16 rows; the thread has two of them, 8 apart, and 16
-    // of their 64 keys: two neighbours in every group of 8.
+    // A warp's quarter holds 16 rows; the thread has two of them, 8 apart, and
+    // KT / 4 keys of each: two neighbours in every group of 8.
+    constexpr int kG = KT / 8;
     const int r0 = warp * 16 + (lane >> 2);
     const bool has_rows = warp * 16 < NR;  // warp-uniform
     const uint32_t ts = tmem + ((uint32_t)(warp * 32) << 16);
     const float sl2 = a.scale_log2;
     // where this lane's 16-byte row of P goes in a store of four 8x8 pieces
     const int pr = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-    const uint32_t pdst = sbase + SH::kOffP + (pr >> 3) * 1024 + (pr & 7) * 128;
+    const uint32_t prow = (pr >> 3) * 1024 + (pr & 7) * 128;
     uint32_t g = 0, item = 0;
-    while (walk.next(a, first_row)) {
+    while (walk.next()) {
       const Seq x = walk.x;
+      const int first_row = walk.first_row;
       const int nrow = min(NR, x.Q * H - first_row);
       bool valid[2];
       int limit[2];  // last key the row sees
@@ -447,30 +482,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = walk.t0; j < walk.t1; ++j, ++g) {
         // after a failed wait the loop runs on without waiting, so that the
         // four warps keep meeting at their barrier
-        ok = warp_wait(kSFull + (g & 1), (g >> 1) & 1) && ok;
+        ok = ok && warp_wait(kSFull + (g & 1), (g >> 1) & 1);
         tc_fence_after();
         float alpha[2] = {1.f, 1.f};
         bool need = false;
-        uint32_t s[32], w[16];
+        uint32_t s[4 * kG], w[2 * kG];
         if (has_rows) {
-          tmem_ld16x64(ts + (g & 1) * kKeys, s);
+          tmem_ld_s(ts + (g & 1) * KT, s);
           tmem_wait_ld();
         }
         tc_fence_before();  // S has been read
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kSEmpty + (g & 1)]);
         if (has_rows) {
-          const int kt = j * kKeys;
-          if (kt + kKeys - 1 > limit_lo) {
+          const int kt = j * KT;
+          if (kt + KT - 1 > limit_lo) {
             const int k0 = kt + 2 * (lane & 3);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 4 * kG; ++i)
               if (k0 + 8 * (i >> 2) + (i & 1) > limit[(i >> 1) & 1]) s[i] = __float_as_uint(-INFINITY);
           }
           // the two rows side by side, so that their chains overlap
           float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < kG; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               mx[i] = fmax3(mx[i], __uint_as_float(s[4 * k + 2 * i]), __uint_as_float(s[4 * k + 2 * i + 1]));
@@ -496,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the sum takes the unrounded weights, the product P rounded to 16
           // bits: half a step a weight, of the size of the result's own rounding
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < kG; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float2 v = make_float2(__uint_as_float(s[4 * k + 2 * i]), __uint_as_float(s[4 * k + 2 * i + 1]));
@@ -510,13 +545,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool rest = j > walk.t0;
         if (rest && has_rows && (lane & 3) == 0) {
-          rowf[(g & 1) * 64 + r0] = alpha[0];
-          rowf[(g & 1) * 64 + r0 + 8] = alpha[1];
+          row_alpha[(g & 1) * 64 + r0] = alpha[0];
+          row_alpha[(g & 1) * 64 + r0 + 8] = alpha[1];
         }
         const bool any = vote_any(need) && rest;
-        // P(j-1) and O are free once the second product of tile j-1 is done
-        if (g > 0) ok = warp_wait(kPvDone, (g - 1) & 1) && ok;
+        ok = ok && warp_wait(kPvDone + (g & 1), ((g >> 1) & 1) ^ 1);  // tile g-2 has read this buffer of P
         if (any) {
+          ok = ok && warp_wait(kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);  // O is at rest
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < SH::kMTiles * NR / 16; ++c) {
@@ -525,21 +560,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * rowf[(g & 1) * 64 + (c * 16 + i) % NR]);
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * row_alpha[(g & 1) * 64 + (c * 16 + i) % NR]);
             tmem_st16(ts + kTmemO + c * 16, o);
           }
           tmem_wait_st();
         }
         if (has_rows) {
+          const uint32_t pdst = sbase + SH::kOffP + prow + (KT == 64 ? (g & 1) * SH::kPNext : 0);
+          const int c0 = KT == 64 ? 0 : (g & 1) * 4 /* the row's half */;
 #pragma unroll
-          for (int k = 0; k < 8; k += 2)  // pieces: rows 0-7 and 8-15 of keys 8k.., then of keys 8(k+1)..
-            stsm_x4(pdst + (((k + (lane >> 4)) ^ (pr & 7)) << 4), w[2 * k], w[2 * k + 1], w[2 * k + 2], w[2 * k + 3]);
+          for (int k = 0; k < kG; k += 2)  // pieces: rows 0-7 and 8-15 of keys 8k.., then of keys 8(k+1)..
+            stsm_x4(pdst + (((c0 + k + (lane >> 4)) ^ (pr & 7)) << 4), w[2 * k], w[2 * k + 1], w[2 * k + 2],
+                    w[2 * k + 3]);
         }
         // slots past the last key: zero their values (P is 0 there, but 0 * NaN is not)
-        if ((j + 1) * kKeys > x.L) {
+        if ((j + 1) * KT > x.L) {
           const uint32_t cst = sbase + SH::kOffStage + (g % SH::kStages) * SH::kStage;
-          const int z0 = x.L - j * kKeys;
-          for (int i = z0 * (R / 8) + tid; i < kKeys * (R / 8); i += 128) {
+          const int z0 = x.L - j * KT;
+          for (int i = z0 * (R / 8) + tid; i < KT * (R / 8); i += 128) {
             const int key = i / (R / 8), v = i % (R / 8);
             st_shared_v4(cst + (key >> 3) * SH::kGroup + (v >> 3) * 1024 + (key & 7) * 128 + (v & 7) * 16, 0, 0,
                          0, 0);
@@ -548,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
         tc_fence_before();         // stores to O -> the issuing thread
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kPFull]);
+        if (lane == 0) mbar_arrive(&bars[kPFull + (g & 1)]);
       }
       // ---- epilogue ----
 #pragma unroll
@@ -556,18 +594,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       }
-      ok = warp_wait(kPvDone, (g - 1) & 1) && ok;
+      ok = ok && warp_wait(kPvDone + ((g - 1) & 1), ((g - 1) >> 1) & 1);
       tc_fence_after();
       const bool whole = walk.t0 == 0 && walk.t1 == x.tiles;
       const bool bad = words[kWBad + item % kBadSlots] == (int)item + 1 || !ok;
       const int64_t row0 = (int64_t)x.q0 * H + first_row;
-      const int64_t slot = ((int64_t)worker * 2 + (walk.t0 == 0 ? 1 : 0)) * row_tiles + rt;
+      const int64_t slot = ((int64_t)worker * 2 + (walk.t0 == 0 ? 1 : 0)) * line.lanes + rt;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = r0 + 8 * i;
         if (!valid[i] || (lane & 3)) continue;
         if (whole) {
-          rowf[r] = l[i] > 0.f ? 1.f / l[i] : (l[i] != l[i] ? l[i] : 0.f);
+          row_inv[(item & 1) * 64 + r] = l[i] > 0.f ? 1.f / l[i] : (l[i] != l[i] ? l[i] : 0.f);
           if (a.lse)
             a.lse[row0 + r] = bad ? -INFINITY : l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f
                                               : (l[i] != l[i] ? l[i] : -INFINITY);
@@ -577,22 +615,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       named_sync(1, 128);
-      constexpr int kW = NR < 32 ? NR : 32;  // columns a load
-      for (int mt = 0; mt < SH::kMTiles; ++mt) {
-        const int dim = mt * 128 + warp * 32 + lane;
+      const volatile float *inv = row_inv + (item & 1) * 64;
+      constexpr int kC = SH::kMTiles * NR;  // columns of O^T: 128 values a row, tile after tile
+      constexpr int kW = kC < 64 ? kC : 64;  // read at once
 #pragma unroll 1
-        for (int n0 = 0; n0 < NR; n0 += kW) {
-          if (n0 >= nrow) break;  // warp-uniform
-          uint32_t o[kW];
-          tmem_ld_cols(ts + kTmemO + mt * NR + n0, o);
-          tmem_wait_ld();
+      for (int c0 = 0; c0 < kC; c0 += kW) {
+        uint32_t o[kW / 16][16];
+#pragma unroll
+        for (int c = 0; c < kW / 16; ++c) tmem_ld16(ts + kTmemO + c0 + c * 16, o[c]);
+        tmem_wait_ld();
+        if (c0 + kW == kC) {  // O may be written again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kOFree]);
+        }
+#pragma unroll
+        for (int c = 0; c < kW / 16; ++c) {
+          const int n0 = (c0 + c * 16) % NR;
+          const int dim = (c0 + c * 16) / NR * 128 + warp * 32 + lane;
+          if (n0 >= nrow) continue;  // warp-uniform
           if (whole) {
             // neighbouring lanes exchange, so that each stores two values of a row
 #pragma unroll
-            for (int i = 0; i < kW; i += 2) {
-              const float f0 = rowf[n0 + i], f1 = rowf[n0 + i + 1];
-              const float v0 = bad || f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0;
-              const float v1 = bad || f1 == 0.f ? 0.f : __uint_as_float(o[i + 1]) * f1;
+            for (int i = 0; i < 16; i += 2) {
+              const float f0 = inv[n0 + i], f1 = inv[n0 + i + 1];
+              const float v0 = bad || f0 == 0.f ? 0.f : __uint_as_float(o[c][i]) * f0;
+              const float v1 = bad || f1 == 0.f ? 0.f : __uint_as_float(o[c][i + 1]) * f1;
               const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
               const int n = n0 + i + (lane & 1);
               const uint32_t two = (lane & 1) ? TT::pack(other, v1) : TT::pack(v0, other);
@@ -601,14 +649,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < kW; ++i)
-              if (n0 + i < nrow) rec[(slot * NR + n0 + i) * R + dim] = __uint_as_float(o[i]);
+            for (int i = 0; i < 16; ++i)
+              if (n0 + i < nrow) rec[(slot * NR + n0 + i) * R + dim] = __uint_as_float(o[c][i]);
           }
         }
       }
-      tc_fence_before();
-      named_sync(1, 128);  // rowf is rewritten by the next item
-      if (lane == 0) mbar_arrive(&bars[kOFree]);
       ++item;
     }
   }
@@ -629,8 +674,8 @@ constexpr int kMaxPieces = 512;
 constexpr int kMergeWarps = 8;
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-    latent_merge_kernel(const LatentArgs a, const float *rec, const float *rec_ml, const int *pref, int workers,
-                        int row_tiles, int NR, int rows_per_cta) {
+    latent_merge_kernel(const LatentArgs a, const float *rec, const float *rec_ml, const int *pref,
+                        const Line line, int rows_per_cta) {
   constexpr int V = R / 128;  // float4 a lane: values lane * 4 + 128 v
   __shared__ float4 so[kMergeWarps][R / 4];
   __shared__ float sl[kMergeWarps];
@@ -638,22 +683,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int per_seq = (a.max_query_len * a.num_heads + rows_per_cta - 1) / rows_per_cta;
   const int s = blockIdx.x / per_seq;
-  const Seq x = seq_of(a, s, nullptr);
+  const Seq x = seq_of(a, line, s, nullptr);
   const int rows = x.Q * a.num_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = pref[a.num_seqs], p0 = pref[s];
-  workers = min(workers, total);
-  auto owner = [&](int t) { return (int)((((int64_t)t + 1) * workers - 1) / total); };
-  const int w0 = x.tiles ? owner(p0) : 0, w1 = x.tiles ? owner(p0 + x.tiles - 1) : 0;
-  if (x.tiles && w0 == w1) return;  // written by its worker
-  const int np = x.tiles ? w1 - w0 + 1 : 0;
+  const int workers = min(line.workers, total);
+  auto owner = [&](int u) { return (int)((((int64_t)u + 1) * workers - 1) / total); };
+  if (x.tiles && owner(p0) == owner(p0 + line.units(x, a.num_heads) - 1)) return;  // written by its worker
   const bool shared_row = rows_per_cta == 1;
   const int step = shared_row ? kMergeWarps : 1;
   for (int base = (int)(blockIdx.x % per_seq) * rows_per_cta; base < rows; base += per_seq * rows_per_cta) {
     const int row = base + (shared_row ? 0 : warp);
     if (row >= rows) break;  // a whole warp, and only where no barrier follows
-    const int rt = row / NR, r = row % NR;
+    const int rt = row / line.nr, r = row % line.nr;
+    // units of the row's tiles, and the workers that hold them
+    const int u0 = p0 + kItemTiles + (line.flat ? rt * (x.tiles + kItemTiles) : 0);
+    const int w0 = x.tiles ? owner(u0) : 0, w1 = x.tiles ? owner(u0 + x.tiles - 1) : 0;
+    const int np = x.tiles ? w1 - w0 + 1 : 0;
+    if (np == 1) continue;  // written by its worker (uniform where barriers follow: one row a CTA)
     // record of the i-th piece: the first starts the sequence, the others continue it
-    auto at = [&](int i) { return ((((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * row_tiles + rt) * NR + r); };
+    auto at = [&](int i) { return ((((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * line.lanes + (line.flat ? 0 : rt)) * line.nr + r); };
     float M = -INFINITY;
     for (int i = lane; i < np; i += 32) M = fmaxf(M, rec_ml[at(i) * 2]);
 #pragma unroll
@@ -720,21 +768,29 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 }
 
 struct Plan {
-  int nr, row_tiles, workers;
+  Line line;
+  int row_tiles;
   size_t pref, ml, rec, total;  // workspace offsets
 };
 
-Plan plan_of(int num_seqs, int max_query_len, int num_heads, int latent_dim, int sm_count) {
+// Keys a tile: 32 where a row is long (512 values), so that four or five tiles
+// fit and the next ones are on their way while one is worked on; 64 halve the
+// waits per key where four of those fit.
+constexpr int key_tile(int latent_dim) { return latent_dim == 512 ? 32 : 64; }
+
+Plan plan_of(int num_seqs, int max_query_len, int num_heads, int latent_dim, int ragged, int sm_count) {
   Plan p;
   const int64_t rows = (int64_t)max_query_len * num_heads;
   // rows a CTA holds: fewer cost less in the second product (its N) and leave
   // shared memory for the keys
-  p.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  p.row_tiles = (int)((rows + p.nr - 1) / p.nr);
-  p.workers = sm_count / p.row_tiles;
-  if (p.workers < 1) p.workers = 1;
-  if (p.workers > kMaxPieces) p.workers = kMaxPieces;
-  const size_t recs = p.workers > 1 ? (size_t)p.workers * 2 * p.row_tiles * p.nr : 0;
+  p.line.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  p.line.kt = key_tile(latent_dim);
+  p.row_tiles = (int)((rows + p.line.nr - 1) / p.line.nr);
+  p.line.flat = ragged && p.row_tiles > 1;
+  p.line.lanes = p.line.flat ? 1 : p.row_tiles;
+  p.line.workers = sm_count / p.line.lanes;
+  if (p.line.workers < 1) p.line.workers = 1;
+  const size_t recs = p.line.workers > 1 ? (size_t)p.line.workers * 2 * p.line.lanes * p.line.nr : 0;
   p.pref = 0;
   p.ml = ((size_t)(num_seqs + 1) * 4 + 255) / 256 * 256;
   p.rec = p.ml + (recs * 8 + 255) / 256 * 256;
@@ -742,9 +798,9 @@ Plan plan_of(int num_seqs, int max_query_len, int num_heads, int latent_dim, int
   return p;
 }
 
-template <typename T, int R, int NR, int BS>
+template <typename T, int R, int NR, int KT, int BS>
 cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
-  using SH = Shape<R, NR>;
+  using SH = Shape<R, NR, KT>;
   auto fn = encode_fn_tc();
   if (!fn) return cudaErrorNotSupported;
   CUtensorMap tmq, tmc;
@@ -763,7 +819,7 @@ cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
     // [8-key group][piece][8 keys][64 values], innermost first below
     cuuint64_t dims[4] = {64, 8, (cuuint64_t)SH::kPieces, (cuuint64_t)a.num_blocks * (BS / 8)};
     cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16};
-    cuuint32_t box[4] = {64, 8, (cuuint32_t)SH::kPieces, (cuuint32_t)(BS / 8)};
+    cuuint32_t box[4] = {64, 8, (cuuint32_t)SH::kPieces, (cuuint32_t)((BS < KT ? BS : KT) / 8)};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     r = fn(&tmc, TcType<T>::kTma, 4, const_cast<void *>(a.cache), dims, strides, box, estr,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -773,7 +829,7 @@ cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
     debug_log("latent_decode: tensor map refused (CUresult %d)", (int)r);
     return cudaErrorInvalidValue;
   }
-  auto kern = latent_decode_kernel<T, R, NR, BS>;
+  auto kern = latent_decode_kernel<T, R, NR, KT, BS>;
   cudaError_t e = set_smem_limit_once(reinterpret_cast<const void *>(kern), SH::kSmem, true);
   if (e != cudaSuccess) return e;
   char *ws = static_cast<char *>(a.ws);
@@ -786,10 +842,10 @@ cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  cfg.gridDim = dim3((unsigned)(p.workers * p.row_tiles));
+  cfg.gridDim = dim3((unsigned)(p.line.workers * p.line.lanes));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = SH::kSmem;
-  e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmc, rec, ml, pref, p.workers, p.row_tiles);
+  e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmc, rec, ml, pref, p.line);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.max_query_len * a.num_heads;
   const int rows_per_cta = a.num_seqs * rows >= 4096 ? kMergeWarps : 1;
@@ -797,32 +853,40 @@ cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, latent_merge_kernel<T, R>, a, (const float *)rec, (const float *)ml,
-                            (const int *)pref, p.workers, p.row_tiles, p.nr, rows_per_cta);
+                            (const int *)pref, p.line, rows_per_cta);
 }
 
 template <typename T, int R, int NR>
 cudaError_t launch_bs(const LatentArgs &a, const Plan &p, cudaStream_t s) {
-  if (a.block_size == 16) return launch_t<T, R, NR, 16>(a, p, s);
-  if (a.block_size == 32) return launch_t<T, R, NR, 32>(a, p, s);
-  return launch_t<T, R, NR, 64>(a, p, s);
+  if (a.block_size == 16) return launch_t<T, R, NR, key_tile(R), 16>(a, p, s);
+  if (a.block_size == 32) return launch_t<T, R, NR, key_tile(R), 32>(a, p, s);
+  return launch_t<T, R, NR, key_tile(R), 64>(a, p, s);
 }
 
 template <typename T, int R>
 cudaError_t launch_nr(const LatentArgs &a, const Plan &p, cudaStream_t s) {
-  if (p.nr == 16) return launch_bs<T, R, 16>(a, p, s);
-  if (p.nr == 32) return launch_bs<T, R, 32>(a, p, s);
+  if (p.line.nr == 16) return launch_bs<T, R, 16>(a, p, s);
+  if (p.line.nr == 32) return launch_bs<T, R, 32>(a, p, s);
   return launch_bs<T, R, 64>(a, p, s);
 }
 
 }  // namespace
 
 size_t latent_decode_ws(int num_seqs, int max_query_len, int num_heads, int latent_dim, int sm_count) {
-  return plan_of(num_seqs, max_query_len, num_heads, latent_dim, sm_count).total;
+  const size_t even = plan_of(num_seqs, max_query_len, num_heads, latent_dim, 0, sm_count).total;
+  const size_t ragged = plan_of(num_seqs, max_query_len, num_heads, latent_dim, 1, sm_count).total;
+  return even > ragged ? even : ragged;
+}
+
+bool latent_decode_fits(int num_seqs, int max_query_len, int num_heads, int latent_dim, int max_context_len) {
+  const Plan p = plan_of(num_seqs, max_query_len, num_heads, latent_dim, 1, 1);
+  const int64_t per = (int64_t)(max_context_len / p.line.kt + 1 + kItemTiles) * p.row_tiles;
+  return per <= INT_MAX / num_seqs && (int64_t)num_seqs * max_query_len * num_heads <= INT_MAX;
 }
 
 cudaError_t launch_latent_decode(const LatentArgs &a, int dtype, int sm_count, cudaStream_t stream) {
-  if ((int64_t)a.num_seqs * a.max_query_len * a.num_heads > 0x7fffffff) return cudaErrorInvalidValue;
-  const Plan p = plan_of(a.num_seqs, a.max_query_len, a.num_heads, a.latent_dim, sm_count);
+  const Plan p = plan_of(a.num_seqs, a.max_query_len, a.num_heads, a.latent_dim, a.query_start_loc != nullptr,
+                         sm_count);
   if (dtype == PA_BF16)
     return a.latent_dim == 512 ? launch_nr<__nv_bfloat16, 512>(a, p, stream)
                                : launch_nr<__nv_bfloat16, 256>(a, p, stream);

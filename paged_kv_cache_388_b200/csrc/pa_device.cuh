@@ -78,18 +78,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
   return true;
 }
 
-// The same wait for short expected times: the clock, whose read takes longer
-// than a poll, is looked at on every 64th.
-__device__ __forceinline__ bool mbar_wait_spin(uint64_t *bar, uint32_t parity) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (globaltimer_ns() - t0 <= kWaitLimitNs)
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-  return false;
-}
-
 // Wait (each wait bounded) until the copies into the last `issued` uses of a
 // ring of `stages` full barriers have landed: use i of the ring is stage
 // i % stages in phase (i / stages) & 1.  A use that was only arrived on
