@@ -111,20 +111,24 @@ def library():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle, without a Stream object
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _dev(t, name, dtype=None):
+def _dev(t, name, dtype=None, cur=None):
     """A contiguous CUDA tensor on the current device (the library launches on
-    the current device and would otherwise dereference another GPU's memory)."""
+    the current device and would otherwise dereference another GPU's memory).
+    ``cur``: that device's index, where the caller has read it."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
+    if cur is None:
+        cur = torch.cuda.current_device()
     if t.device.index != cur:
         raise ValueError(f"{name} is on {t.device} but the current device is cuda:{cur}; "
                          "call under torch.cuda.device(...) of the tensors' device")
@@ -460,26 +464,38 @@ def pa_decode_shared_prefix_fp8(out, q, k_cache, v_cache, block_tables, context_
     _check(rc, "pa_decode_shared_prefix_fp8")
 
 
-def _dev_rows(t, name, dtype):
+def _here(t, name):
+    """The current device's index, read once a call (t: any of its tensors)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _dev_rows(t, name, dtype, cur):
     """A CUDA tensor on the current device whose last dimension is contiguous;
     returns its element strides before it (a dimension of one row or head
     counts as packed: torch leaves its stride arbitrary)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device} but the current device is "
-                         f"cuda:{torch.cuda.current_device()}; call under torch.cuda.device(...)")
+    if t.device.index != cur:
+        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{cur}; "
+                         "call under torch.cuda.device(...) of the tensors' device")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    strides, packed = [], 1
-    for n, st in zip(reversed(t.shape), reversed(t.stride())):
-        strides.append(st if n > 1 else packed)
-        packed *= max(n, 1)
-    if strides[0] != 1:
+    shape, strides = t.shape, list(t.stride())
+    packed = 1
+    for i in range(len(shape) - 1, -1, -1):
+        if shape[i] <= 1:
+            strides[i] = packed
+        packed *= max(shape[i], 1)
+    if strides[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    if any(x % 8 for x in strides[1:]) or t.data_ptr() % 16:
+    for st in strides[:-1]:
+        if st % 8:
+            raise ValueError(f"rows of {name} must start on 16-byte boundaries")
+    if t.data_ptr() % 16:
         raise ValueError(f"rows of {name} must start on 16-byte boundaries")
-    return strides[:0:-1]
+    return strides[:-1]
 
 
 def _latent_shape(latent_cache):
@@ -499,10 +515,11 @@ def pa_latent_write(latent, rope, latent_cache, slot_mapping, stream=None):
            f"latent and rope rows must add up to the cache's {w} values")
     _shape(slot_mapping.dim() == 1 and slot_mapping.shape[0] == latent.shape[0],
            "slot_mapping must hold one slot per token")
-    _dev(latent_cache, "latent_cache")
-    ls, = _dev_rows(latent, "latent", latent_cache.dtype)
-    rs, = _dev_rows(rope, "rope", latent_cache.dtype)
-    _dev(slot_mapping, "slot_mapping", torch.int64)
+    cur = _here(latent_cache, "latent_cache")
+    _dev(latent_cache, "latent_cache", None, cur)
+    ls, = _dev_rows(latent, "latent", latent_cache.dtype, cur)
+    rs, = _dev_rows(rope, "rope", latent_cache.dtype, cur)
+    _dev(slot_mapping, "slot_mapping", torch.int64, cur)
     rc = _lib.pa_latent_write(_ptr(latent), _ptr(rope), _ptr(latent_cache), _ptr(slot_mapping),
                               latent.shape[0], ls, rs, latent.shape[1], rope.shape[1], bs, nb,
                               _DT.get(latent_cache.dtype, -1), _stream(stream))
@@ -536,16 +553,18 @@ def pa_latent_decode(out, lse, q, latent_cache, block_tables, context_lens, scal
     else:
         _shape(query_start_loc.dim() == 1 and query_start_loc.shape[0] == s + 1,
                "query_start_loc must have num_seqs + 1 entries")
-        _dev(query_start_loc, "query_start_loc", torch.int32)
-    _dev(q, "q")
-    _dev(out, "out", q.dtype)
-    _dev(latent_cache, "latent_cache", q.dtype)
-    _dev(block_tables, "block_tables", torch.int32)
-    _dev(context_lens, "context_lens", torch.int32)
+    cur = _here(q, "q")
+    if query_start_loc is not None:
+        _dev(query_start_loc, "query_start_loc", torch.int32, cur)
+    _dev(q, "q", None, cur)
+    _dev(out, "out", q.dtype, cur)
+    _dev(latent_cache, "latent_cache", q.dtype, cur)
+    _dev(block_tables, "block_tables", torch.int32, cur)
+    _dev(context_lens, "context_lens", torch.int32, cur)
     if lse is not None:
-        _dev(lse, "lse", torch.float32)
+        _dev(lse, "lse", torch.float32, cur)
     if workspace is not None:
-        _dev(workspace, "workspace")
+        _dev(workspace, "workspace", None, cur)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = _lib.pa_latent_decode(_ptr(out), _ptr(lse), _ptr(q), _ptr(latent_cache),
                                _ptr(block_tables), mbps, _ptr(context_lens), _ptr(query_start_loc),
@@ -573,15 +592,16 @@ def pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_
     _shape(query_start_loc.dim() == 1 and query_start_loc.shape[0] >= 1 and
            query_start_loc.shape == context_start_loc.shape,
            "query_start_loc and context_start_loc must have num_seqs + 1 entries each")
-    _dev(q, "q")
-    _dev(out, "out", q.dtype)
-    ks, kh = _dev_rows(k, "k", q.dtype)
-    vs, vh = _dev_rows(v, "v", q.dtype)
-    krs, = _dev_rows(k_rope, "k_rope", q.dtype)
+    cur = _here(q, "q")
+    _dev(q, "q", None, cur)
+    _dev(out, "out", q.dtype, cur)
+    ks, kh = _dev_rows(k, "k", q.dtype, cur)
+    vs, vh = _dev_rows(v, "v", q.dtype, cur)
+    krs, = _dev_rows(k_rope, "k_rope", q.dtype, cur)
     if lse is not None:
-        _dev(lse, "lse", torch.float32)
-    _dev(query_start_loc, "query_start_loc", torch.int32)
-    _dev(context_start_loc, "context_start_loc", torch.int32)
+        _dev(lse, "lse", torch.float32, cur)
+    _dev(query_start_loc, "query_start_loc", torch.int32, cur)
+    _dev(context_start_loc, "context_start_loc", torch.int32, cur)
     rc = _lib.pa_latent_prefill(_ptr(out), _ptr(lse), _ptr(q), _ptr(k), _ptr(k_rope), _ptr(v),
                                 ks, kh, krs, vs, vh, _ptr(query_start_loc),
                                 _ptr(context_start_loc), query_start_loc.shape[0] - 1, tq, tk,
@@ -595,18 +615,21 @@ def _table_shapes(block_tables, context_lens, ref_counts):
     _shape(tuple(context_lens.shape) == (block_tables.shape[0],),
            "block_tables and context_lens disagree on the number of sequences")
     _shape(ref_counts.dim() == 1, "ref_counts must be [num_blocks]")
-    _dev(block_tables, "block_tables", torch.int32)
-    _dev(context_lens, "context_lens", torch.int32)
-    _dev(ref_counts, "ref_counts", torch.int32)
-    return (*block_tables.shape, ref_counts.shape[0])
+    cur = _here(block_tables, "block_tables")
+    _dev(block_tables, "block_tables", torch.int32, cur)
+    _dev(context_lens, "context_lens", torch.int32, cur)
+    _dev(ref_counts, "ref_counts", torch.int32, cur)
+    return (*block_tables.shape, ref_counts.shape[0], cur)
 
 
-def _pool_args(pools, num_blocks):
+def _pool_args(pools, num_blocks, cur):
     """Host arrays of the pools' addresses and block bytes."""
     n = len(pools)
-    ptrs, sizes = (P * max(n, 1))(), (L * max(n, 1))()
+    if n == 0:
+        return None, None, 0
+    ptrs, sizes = (P * n)(), (L * n)()
     for i, t in enumerate(pools):
-        _dev(t, "pool")
+        _dev(t, "pool", None, cur)
         _shape(t.dim() >= 1 and t.shape[0] == num_blocks,
                f"a pool must hold {num_blocks} blocks, got {tuple(t.shape)}")
         ptrs[i] = t.data_ptr()
@@ -625,21 +648,21 @@ def pa_table_step(block_tables, context_lens, ref_counts, append, block_size, sl
     [NB], updated in place; append, release, fork_src int32 [S]; slot_mapping
     int64 [max_new_tokens], query_start_loc int32 [S + 1] and copy_pairs int64
     [S, 2] are written; pools: CUDA tensors [NB, ...] whose blocks follow."""
-    s, w, nb = _table_shapes(block_tables, context_lens, ref_counts)
+    s, w, nb, cur = _table_shapes(block_tables, context_lens, ref_counts)
     for name, t in (("append", append), ("release", release), ("fork_src", fork_src)):
         if t is not None:
             _shape(tuple(t.shape) == (s,), f"{name} must hold one entry per sequence")
-            _dev(t, name, torch.int32)
+            _dev(t, name, torch.int32, cur)
     _shape(slot_mapping.dim() == 1, "slot_mapping must be [max_new_tokens]")
     _shape(tuple(query_start_loc.shape) == (s + 1,),
            "query_start_loc must have num_seqs + 1 entries")
     _shape(tuple(copy_pairs.shape) == (s, 2), "copy_pairs must be [num_seqs, 2]")
-    _dev(slot_mapping, "slot_mapping", torch.int64)
-    _dev(query_start_loc, "query_start_loc", torch.int32)
-    _dev(copy_pairs, "copy_pairs", torch.int64)
-    ptrs, sizes, n = _pool_args(pools, nb)
+    _dev(slot_mapping, "slot_mapping", torch.int64, cur)
+    _dev(query_start_loc, "query_start_loc", torch.int32, cur)
+    _dev(copy_pairs, "copy_pairs", torch.int64, cur)
+    ptrs, sizes, n = _pool_args(pools, nb, cur)
     if workspace is not None:
-        _dev(workspace, "workspace")
+        _dev(workspace, "workspace", None, cur)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = _lib.pa_table_step(_ptr(block_tables), w, _ptr(context_lens), _ptr(ref_counts),
                             _ptr(release), _ptr(fork_src), _ptr(append), s, nb, int(block_size),
@@ -654,15 +677,15 @@ def pa_table_compact(block_tables, context_lens, ref_counts, block_size, num_liv
     """Move the used blocks to ids [0, live): block_tables, ref_counts and the
     pools' blocks are updated in place; num_live int32 [1] and block_moves
     int64 [max(1, NB // 2), 2] are written."""
-    s, w, nb = _table_shapes(block_tables, context_lens, ref_counts)
+    s, w, nb, cur = _table_shapes(block_tables, context_lens, ref_counts)
     _shape(tuple(num_live.shape) == (1,), "num_live must be [1]")
     _shape(tuple(block_moves.shape) == (max(1, nb // 2), 2),
            "block_moves must be [max(1, num_blocks // 2), 2]")
-    _dev(num_live, "num_live", torch.int32)
-    _dev(block_moves, "block_moves", torch.int64)
-    ptrs, sizes, n = _pool_args(pools, nb)
+    _dev(num_live, "num_live", torch.int32, cur)
+    _dev(block_moves, "block_moves", torch.int64, cur)
+    ptrs, sizes, n = _pool_args(pools, nb, cur)
     if workspace is not None:
-        _dev(workspace, "workspace")
+        _dev(workspace, "workspace", None, cur)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = _lib.pa_table_compact(_ptr(block_tables), w, _ptr(context_lens), _ptr(ref_counts), s, nb,
                                int(block_size), _ptr(num_live), _ptr(block_moves), ptrs, sizes, n,

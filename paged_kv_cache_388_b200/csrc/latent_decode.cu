@@ -243,16 +243,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBadSlots; ++i) words[kWBad + i] = 0;
     mbar_init_fence();
   }
+  if (tid == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmq)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmc)) : "memory");
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the worker's range of units -----------------------------------------
   volatile int *scan = words + kWScan;
   unsigned int *err0 = blockIdx.x == 0 ? a.err : nullptr;
-  int sum = 0;
-  for (int s = tid; s < a.num_seqs; s += kThreads) sum += line.units(seq_of(a, line, s, err0), H);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const int n_first = tid < a.num_seqs ? line.units(seq_of(a, line, tid, err0), H) : 0;
+  int sum = n_first;
+  for (int s = tid + kThreads; s < a.num_seqs; s += kThreads) sum += line.units(seq_of(a, line, s, err0), H);
+  sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) scan[warp] = sum;
   __syncthreads();
   int total = 0;
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int base = 0;
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     const int s = s0 + tid;
-    const int n = s < a.num_seqs ? line.units(seq_of(a, line, s, nullptr), H) : 0;
+    const int n = s0 == 0 ? n_first : s < a.num_seqs ? line.units(seq_of(a, line, s, nullptr), H) : 0;
     int x = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -670,7 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // each, when there are rows enough to fill the machine, else one row whose
 // pieces the 8 warps share and join through shared memory (one long sequence
 // is cut into as many pieces as there are workers).
-constexpr int kMaxPieces = 512;
 constexpr int kMergeWarps = 8;
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * kMergeWarps)
@@ -678,16 +681,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
                         const Line line, int rows_per_cta) {
   constexpr int V = R / 128;  // float4 a lane: values lane * 4 + 128 v
   __shared__ float4 so[kMergeWarps][R / 4];
-  __shared__ float sl[kMergeWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ float sm[kMergeWarps], sl[kMergeWarps];
   const int per_seq = (a.max_query_len * a.num_heads + rows_per_cta - 1) / rows_per_cta;
   const int s = blockIdx.x / per_seq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int total = pref[a.num_seqs], p0 = pref[s];
   const Seq x = seq_of(a, line, s, nullptr);
   const int rows = x.Q * a.num_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int total = pref[a.num_seqs], p0 = pref[s];
   const int workers = min(line.workers, total);
-  auto owner = [&](int u) { return (int)((((int64_t)u + 1) * workers - 1) / total); };
+  // the worker of unit u: the last w with total * w / workers <= u
+  const bool narrow = (uint64_t)total * (uint64_t)workers <= 0xffffffffu;
+  auto owner = [&](int u) -> int {
+    return narrow ? (int)((((uint32_t)u + 1) * (uint32_t)workers - 1) / (uint32_t)total)
+                  : (int)((((int64_t)u + 1) * workers - 1) / total);
+  };
   if (x.tiles && owner(p0) == owner(p0 + line.units(x, a.num_heads) - 1)) return;  // written by its worker
   const bool shared_row = rows_per_cta == 1;
   const int step = shared_row ? kMergeWarps : 1;
@@ -701,53 +709,76 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const int np = x.tiles ? w1 - w0 + 1 : 0;
     if (np == 1) continue;  // written by its worker (uniform where barriers follow: one row a CTA)
     // record of the i-th piece: the first starts the sequence, the others continue it
-    auto at = [&](int i) { return ((((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * line.lanes + (line.flat ? 0 : rt)) * line.nr + r); };
-    float M = -INFINITY;
-    for (int i = lane; i < np; i += 32) M = fmaxf(M, rec_ml[at(i) * 2]);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    auto at = [&](int i) {
+      return (((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * line.lanes + (line.flat ? 0 : rt)) * line.nr + r;
+    };
+    // four pieces at a time, joined as they come: maxima and sums are read together
     float4 o[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
+    float M = -INFINITY, l = 0.f;
     bool bad = false;
-#pragma unroll 4
-    for (int i = shared_row ? warp : 0; i < np; i += step) {
-      const int64_t k = at(i);
-      const float2 ml = *reinterpret_cast<const float2 *>(rec_ml + k * 2);
-      float4 p[V];
+    for (int i0 = shared_row ? warp : 0; i0 < np; i0 += 4 * step) {
+      float2 ml[4];
+      float4 p[4][V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) p[v] = __ldcs(reinterpret_cast<const float4 *>(rec + k * R + v * 128 + lane * 4));
-      bad = bad || ml.y < 0.f;
-      // a piece without a visible key has no sums (a NaN total is not one)
-      const bool empty = ml.x == -INFINITY && ml.y <= 0.f;
-      const float f = empty ? 0.f : exp2f(ml.x - M);
-      l += empty ? 0.f : f * ml.y;
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * step;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (i >= np) continue;
+        const int64_t k = at(i);
+        ml[u] = *reinterpret_cast<const float2 *>(rec_ml + k * 2);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        o[v].x += empty ? 0.f : f * p[v].x;
-        o[v].y += empty ? 0.f : f * p[v].y;
-        o[v].z += empty ? 0.f : f * p[v].z;
-        o[v].w += empty ? 0.f : f * p[v].w;
+        for (int v = 0; v < V; ++v) p[u][v] = __ldcs(reinterpret_cast<const float4 *>(rec + k * R + v * 128 + lane * 4));
+      }
+      const float top = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+      const float f0 = M == -INFINITY ? 0.f : exp2f(M - top);
+      M = top;
+      l *= f0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = make_float4(o[v].x * f0, o[v].y * f0, o[v].z * f0, o[v].w * f0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        bad = bad || ml[u].y < 0.f;
+        // a piece without a visible key has no sums (a NaN total is not one)
+        if (ml[u].x == -INFINITY && ml[u].y <= 0.f) continue;
+        const float f = exp2f(ml[u].x - M);
+        l += f * ml[u].y;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o[v].x += f * p[u][v].x;
+          o[v].y += f * p[u][v].y;
+          o[v].z += f * p[u][v].z;
+          o[v].w += f * p[u][v].w;
+        }
       }
     }
     if (shared_row) {  // one row a CTA: the barriers are uniform
       __syncthreads();
 #pragma unroll
       for (int v = 0; v < V; ++v) so[warp][v * 32 + lane] = o[v];
-      if (lane == 0) sl[warp] = bad ? -INFINITY : l;
+      if (lane == 0) {
+        sm[warp] = M;
+        sl[warp] = bad ? -1.f : l;
+      }
       __syncthreads();
       if (warp) continue;
-      for (int w = 1; w < kMergeWarps; ++w) {
-        bad = bad || sl[w] == -INFINITY;
-        l += sl[w];
+      for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, sm[w]);
+      l = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < kMergeWarps; ++w) {
+        bad = bad || sl[w] < 0.f;
+        if (sm[w] == -INFINITY && sl[w] <= 0.f) continue;
+        const float f = exp2f(sm[w] - M);
+        l += f * sl[w];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float4 y = so[w][v * 32 + lane];
-          o[v].x += y.x;
-          o[v].y += y.y;
-          o[v].z += y.z;
-          o[v].w += y.w;
+          o[v].x += f * y.x;
+          o[v].y += f * y.y;
+          o[v].z += f * y.z;
+          o[v].w += f * y.w;
         }
       }
     }

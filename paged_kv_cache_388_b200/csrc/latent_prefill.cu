@@ -151,6 +151,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
   };
 
+  // a wait of a whole warp; the clock, whose read takes longer than a poll, and
+  // the flag of a failure elsewhere are looked at on every 64th
+  auto warp_wait = [&](int bar, uint32_t parity) -> bool {
+    bool ok = false;
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+      const uint64_t start = globaltimer_ns();
+      while (!ok && !*abort_flag && globaltimer_ns() - start <= kWaitLimitNs)
+        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) fail();
+    }
+    return ok;
+  };
+
   if (warp == kProducerWarp) {
     // ======================= producer =======================================
     if (lane == 0) {
@@ -183,71 +198,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ======================= MMA issue ======================================
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = umma_idesc(TT::kFmt, 0, 0, kRows, kKeys);
-      constexpr uint32_t idesc_pv = umma_idesc(TT::kFmt, 0, 1, kRows, 64);
-      auto chunk_full = [&](uint32_t x) { return mbar_wait(&bars[kFull + x % kRing], (x / kRing) & 1); };
-      // S_t(j) = Q_t K_j^T: both K-major, 8-row groups 1 KB apart
-      auto issue_s = [&](int t, int j) -> bool {
-        const uint32_t x0 = (uint32_t)j * SH::kTC;
+    constexpr uint32_t idesc_s = umma_idesc(TT::kFmt, 0, 0, kRows, kKeys);
+    constexpr uint32_t idesc_pv = umma_idesc(TT::kFmt, 0, 1, kRows, 64);
+    constexpr uint32_t kHi = umma_desc_hi(1024);
+    const uint32_t q_lo = umma_desc_lo(sbase, 16), k_lo = umma_desc_lo(ring, 16), v_lo = umma_desc_lo(ring, kChunk);
+    auto chunk_full = [&](uint32_t x) { return warp_wait(kFull + x % kRing, (x / kRing) & 1); };
+    // S_t(j) = Q_t K_j^T: both K-major, 8-row groups 1 KB apart
+    auto issue_s = [&](int t, int j) -> bool {
+      const uint32_t x0 = (uint32_t)j * SH::kTC;
+      for (int c = 0; c < SH::kKC; ++c)
+        if (!chunk_full(x0 + c)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t a_lo = q_lo + t * (SH::kQBytes >> 4), d = tmem + tmem_s_col(t);
+#pragma unroll
         for (int c = 0; c < SH::kKC; ++c) {
-          if (!chunk_full(x0 + c)) return false;
-          tc_fence_after();
-          const uint32_t kst = ring + ((x0 + c) % kRing) * kChunk;
-          const uint32_t qst = sbase + t * SH::kQBytes + c * kChunk;
+          const uint32_t b_lo = k_lo + ((x0 + c) % kRing) * (kChunk >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma(tmem + tmem_s_col(t), umma_desc(qst + kk * 32, 16, 1024), umma_desc(kst + kk * 32, 16, 1024),
-                 idesc_s, (c | kk) ? 1u : 0u);
+            umma_lo(d, a_lo + ((c * kChunk + kk * 32) >> 4), kHi, b_lo + ((kk * 32) >> 4), kHi, idesc_s,
+                    (c | kk) ? 1u : 0u);
         }
         umma_commit(&bars[kSFull + t]);
         if (t == nq - 1)
           for (int c = 0; c < SH::kKC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
-        return true;
-      };
-      // O_t += P_t(j) V_j: A = P from tensor memory (16 keys in 8 columns), B =
-      // V with columns contiguous, 64 of them a product, 8-key groups 1 KB apart
-      auto issue_pv = [&](int t, int j) -> bool {
-        const uint32_t x0 = (uint32_t)j * SH::kTC + SH::kKC;
+      }
+      __syncwarp();
+      return true;
+    };
+    // O_t += P_t(j) V_j: A = P from tensor memory (16 keys in 8 columns), B =
+    // V with columns contiguous, 64 of them a product, 8-key groups 1 KB apart
+    auto issue_pv = [&](int t, int j) -> bool {
+      const uint32_t x0 = (uint32_t)j * SH::kTC + SH::kKC;
+      for (int c = 0; c < SH::kVC; ++c)
+        if (!chunk_full(x0 + c)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t keep = j > 0 ? 1u : 0u;
+#pragma unroll
         for (int c = 0; c < SH::kVC; ++c) {
-          if (!chunk_full(x0 + c)) return false;
-          tc_fence_after();
-          const uint32_t vst = ring + ((x0 + c) % kRing) * kChunk;
+          const uint32_t b_lo = v_lo + ((x0 + c) % kRing) * (kChunk >> 4);
 #pragma unroll
           for (int ks = 0; ks < kKeys / 16; ++ks)
-            umma_ts(tmem + tmem_o_col(t) + c * 64, tmem + tmem_s_col(t) + ks * 8,
-                    umma_desc(vst + ks * 2048, kChunk, 1024), idesc_pv, (j | ks) ? 1u : 0u);
+            umma_ts_lo(tmem + tmem_o_col(t) + c * 64, tmem + tmem_s_col(t) + ks * 8, b_lo + ((ks * 2048) >> 4), kHi,
+                       idesc_pv, ks > 0 ? 1u : keep);
         }
         umma_commit(&bars[kPvDone + t]);
         if (t == nq - 1)
           for (int c = 0; c < SH::kVC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
-        return true;
-      };
-      bool ok = mbar_wait(&bars[kQFull], 0);
-      for (int t = 0; t < nq && ok; ++t)
-        if (t == nq - 1 || nt0 > 0) ok = issue_s(t, 0);
-      for (int j = 0; j < ntiles && ok && !*abort_flag; ++j) {
-        const uint32_t par = (uint32_t)(j & 1);
-        for (int t = 0; t < nq && ok; ++t) {
-          const int nt = t == nq - 1 ? ntiles : nt0;
-          if (j >= nt) continue;
-          ok = mbar_wait(&bars[kPFull + t], par);
-          if (!ok) break;
-          tc_fence_after();
-          ok = issue_pv(t, j);
-          if (ok && j + 1 < nt) {
-            // S(j+1) overwrites P(j) of this Q tile: its P V must be complete
-            ok = mbar_wait(&bars[kPvDone + t], par);
-            if (!ok) break;
-            tc_fence_after();
-            ok = issue_s(t, j + 1);
-          }
-        }
       }
-      if (!ok) fail();
+      __syncwarp();
+      return true;
+    };
+    bool ok = warp_wait(kQFull, 0);
+    for (int t = 0; t < nq && ok; ++t)
+      if (t == nq - 1 || nt0 > 0) ok = issue_s(t, 0);
+    for (int j = 0; j < ntiles && ok; ++j) {
+      const uint32_t par = (uint32_t)(j & 1);
+      for (int t = 0; t < nq && ok; ++t) {
+        const int nt = t == nq - 1 ? ntiles : nt0;
+        if (j >= nt) continue;
+        ok = warp_wait(kPFull + t, par);
+        if (!ok) break;
+        tc_fence_after();
+        ok = issue_pv(t, j);
+        // S(j+1) overwrites P(j) of this Q tile: its P V must be complete
+        if (ok && j + 1 < nt) ok = warp_wait(kPvDone + t, par) && issue_s(t, j + 1);
+      }
+    }
+    if (elect_one()) {
       umma_commit(&bars[kDone]);  // completes when every MMA above has finished
       if (!mbar_wait(&bars[kDone], 0)) fail();
     }
+    __syncwarp();
   } else {
     // ======================= softmax warps ==================================
     const int qt = warp >> 2, qd = warp & 3;
@@ -264,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nt; ++j) {
-        ok = !*abort_flag && mbar_wait(&bars[kSFull + qt], (uint32_t)(j & 1));
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; fail(); break; }  // tcgen05.ld is collective
+        ok = warp_wait(kSFull + qt, (uint32_t)(j & 1));
+        if (!ok) break;
         tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
@@ -347,9 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars[kPFull + qt]);
       }
       // ---- epilogue: O / l -> out ----
-      bool fin = ok && !*abort_flag && (nt == 0 || mbar_wait(&bars[kPvDone + qt], (uint32_t)((nt - 1) & 1)));
-      fin = __all_sync(0xffffffffu, fin);
-      if (!fin) fail();
+      const bool fin = ok && !*abort_flag && (nt == 0 || warp_wait(kPvDone + qt, (uint32_t)((nt - 1) & 1)));
       tc_fence_after();
       const float inv = fin && l > 0.f ? 1.f / l : (l != l ? l : 0.f);
       const bool write = row < ntok;

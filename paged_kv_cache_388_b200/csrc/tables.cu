@@ -7,9 +7,15 @@
 // Both are prefix sums over the pool and over the rows with scattered integer
 // writes around them.  Order decides every result (lowest free id first, rows
 // in order) and no result depends on the order of atomics: reference counts
-// are integer sums.  The kernels of a call are chained with programmatic
-// dependent launches; each waits for its predecessor's writes before it reads
-// anything, so the chain costs little more than its dependent memory trips.
+// are integer sums.
+//
+// Each is one cooperative kernel whose phases are parted by grid barriers: the
+// work of a phase is a few microseconds at most, so that launches would cost
+// more than it (as six dependent launches a step of 256 rows took 15 us on the
+// device and 13 us of the host's time).  What one CTA can sum up in less than
+// a barrier takes -- the counts of the pool's chunks, the needs of the rows --
+// every CTA sums up for itself.
+#include <cooperative_groups.h>
 #include <limits.h>
 
 #include "pa_device.cuh"
@@ -18,15 +24,19 @@
 namespace pa {
 namespace {
 
-constexpr int kChunk = 1024;      // pool blocks per counting CTA (4 a thread)
-constexpr int kThreads = 256;
-constexpr int kPlanThreads = 1024;
-constexpr int kMaxRows = 4096;    // rows the one-CTA plan scans, 4 a thread
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+constexpr int kPerThread = 4;
+constexpr int kChunk = kThreads * kPerThread;  // pool blocks counted at a time
+constexpr int kRowThreads = 128;               // threads that share a row
+constexpr int kRowGroups = kThreads / kRowThreads;
+constexpr int kMaxRows = 4096;
 constexpr int kPoolsPerLaunch = 64;
 
 // Workspace arrays (offsets in bytes, all 256-byte aligned).
 struct TableWs {
-  size_t scal, len, info, base, chunk, list, rows, total;
+  size_t len, writes, info, base, chunk, list, rows, total;
 };
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -35,19 +45,19 @@ TableWs table_ws(int num_seqs, int width, int num_blocks) {
   TableWs w;
   const size_t chunks = ((size_t)num_blocks + kChunk - 1) / kChunk;
   size_t off = 0;
-  w.scal = off;  // [8] ints: total taken, live, moves
-  off += 256;
   w.len = off;  // [num_seqs] length after release and fork
   off += align_up((size_t)num_seqs * 4);
-  w.info = off;  // [num_seqs][2] blocks needed | copy-on-write flag, last block
-  off += align_up((size_t)num_seqs * 8);
+  w.writes = off;  // [num_seqs] block that the row's next token is written into, -1: none held
+  off += align_up((size_t)num_seqs * 4);
+  w.info = off;  // [num_seqs] blocks needed, and whether one is for a copy-on-write
+  off += align_up((size_t)num_seqs * 4);
   w.base = off;  // [num_seqs] first fresh block, -1: not grown
   off += align_up((size_t)num_seqs * 4);
-  w.chunk = off;  // [chunks] counts, then their exclusive prefix
+  w.chunk = off;  // [chunks] counts
   off += align_up(chunks * 4);
   w.list = off;  // step: [num_blocks] fresh ids; compact: remap
   off += align_up((size_t)num_blocks * 4);
-  w.rows = off;  // step: [num_seqs][width] forked rows; compact: [num_blocks] holes and sources
+  w.rows = off;  // step: [num_seqs][width] forked rows; compact: holes and sources, num_blocks / 2 each
   const size_t forked = align_up((size_t)num_seqs * width * 4), lists = align_up((size_t)num_blocks * 4);
   off += forked > lists ? forked : lists;
   w.total = off;
@@ -66,14 +76,9 @@ struct StepArgs {
   int64_t *slots, *pairs;
   int32_t *qsl;
   int S, W, NB, bs, max_new, chunks;
-  int *scal, *wlen, *info, *base, *chunk, *fresh, *wrows;
+  int *wlen, *writes, *info, *base, *chunk, *fresh, *wrows;
   unsigned int *err;
 };
-
-__device__ __forceinline__ void pdl_begin() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 __device__ __forceinline__ int row_len(const int32_t *lens, int i, int cap, unsigned int *err) {
   const int n = lens[i];
@@ -82,8 +87,8 @@ __device__ __forceinline__ int row_len(const int32_t *lens, int i, int cap, unsi
   return 0;
 }
 
-// Exclusive prefix of v over a block of NT threads; *total gets the sum.  s: NT / 32 + 1 entries.
-template <int NT, typename T>
+// Exclusive prefix of v over the block; *total gets the sum.  s: kThreads / 32 + 1 entries.
+template <typename T>
 __device__ __forceinline__ T block_scan(T v, T *s, T *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   T x = v;
@@ -96,251 +101,80 @@ __device__ __forceinline__ T block_scan(T v, T *s, T *total) {
   if (lane == 31) s[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    const T w = lane < NT / 32 ? s[lane] : 0;
+    const T w = lane < kThreads / 32 ? s[lane] : 0;
     T y = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const T z = __shfl_up_sync(0xffffffffu, y, d);
       if (lane >= d) y += z;
     }
-    if (lane < NT / 32) s[lane] = y - w;
-    if (lane == 31) s[NT / 32] = y;
+    if (lane < kThreads / 32) s[lane] = y - w;
+    if (lane == 31) s[kThreads / 32] = y;
   }
   __syncthreads();
-  *total = s[NT / 32];
+  *total = s[kThreads / 32];
   return x - v + s[warp];
 }
 
-// ---- pa_table_step ------------------------------------------------------------
-
-// 1 and 2 of the step: one CTA per row.  Counts change by integer atomics; the
-// blocks of a fork's source are put aside, since its row may itself change.
-__global__ void __launch_bounds__(kThreads) step_release_kernel(const StepArgs a) {
-  pdl_begin();
-  const int i = blockIdx.x, cap = a.W * a.bs;
-  int src = a.fork_src ? a.fork_src[i] : -1;
-  if (src >= a.S) {
-    if (threadIdx.x == 0) raise_error(a.err, PA_DEVERR_TABLE);
-    src = -1;
-  }
-  const bool forked = src >= 0;
-  const bool drop = forked || (a.release && a.release[i] != 0);
-  const int len = row_len(a.lens, i, cap, threadIdx.x == 0 ? a.err : nullptr);
-  int now = drop ? 0 : len;
-  if (drop) {
-    const int32_t *t = a.tables + (int64_t)i * a.W;
-    const int n = (len + a.bs - 1) / a.bs;
-    for (int j = threadIdx.x; j < n; j += kThreads) {
-      const int b = t[j];
-      if (b >= 0 && b < a.NB) atomicSub(a.refs + b, 1);
-      else raise_error(a.err, PA_DEVERR_BLOCK_ID);
-    }
-  }
-  if (forked) {
-    now = row_len(a.lens, src, cap, nullptr);
-    const int32_t *t = a.tables + (int64_t)src * a.W;
-    int *keep = a.wrows + (int64_t)i * a.W;
-    const int n = (now + a.bs - 1) / a.bs;
-    for (int j = threadIdx.x; j < n; j += kThreads) {
-      const int b = t[j];
-      keep[j] = b;
-      if (b >= 0 && b < a.NB) atomicAdd(a.refs + b, 1);
-      else raise_error(a.err, PA_DEVERR_BLOCK_ID);
-    }
-  }
-  if (threadIdx.x == 0) a.wlen[i] = now;
+// A CTA's contiguous share of n chunks.
+__device__ __forceinline__ void chunk_range(int n, int *c0, int *c1) {
+  const int per = (n + (int)gridDim.x - 1) / (int)gridDim.x;
+  *c0 = min(n, (int)blockIdx.x * per);
+  *c1 = min(n, *c0 + per);
 }
 
-// The block that row r's next token is written into when its last block is
-// partly filled, else -1.
-__device__ __forceinline__ int write_block(const StepArgs &a, int r) {
-  const int add = a.append[r], now = a.wlen[r];
-  if (add <= 0 || now % a.bs == 0 || (int64_t)now + add > (int64_t)a.W * a.bs) return -1;
-  const int src = a.fork_src ? a.fork_src[r] : -1;
-  const int *t = src >= 0 && src < a.S ? a.wrows + (int64_t)r * a.W : a.tables + (int64_t)r * a.W;
-  const int b = t[now / a.bs];
-  return b >= 0 && b < a.NB ? b : -1;
+// Sums of the chunk counts: all of them, and those before c0.
+__device__ __forceinline__ void sum_chunks(const int *chunk, int n, int c0, int *s, int *all, int *before) {
+  int x = 0, y = 0;
+  for (int c = threadIdx.x; c < n; c += kThreads) {
+    const int v = chunk[c];
+    x += v;
+    if (c < c0) y += v;
+  }
+  block_scan(x, s, all);
+  block_scan(y, s, before);
 }
 
-// The first `chunks` CTAs count the pool's free blocks; the others take a row
-// each: the forked rows' entries go into the tables and the row's need is
-// worked out.  Of the rows that write into one shared block, in row order, all
-// copy it but the last of its holders: the k-th writer of a block with r
-// holders copies while r - k > 1.
-__global__ void __launch_bounds__(kThreads) step_count_kernel(const StepArgs a) {
-  __shared__ int s[kThreads / 32 + 1];
-  pdl_begin();
-  int total;
-  if ((int)blockIdx.x < a.chunks) {
-    const int id = blockIdx.x * kChunk + threadIdx.x * 4;
-    int n = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (id + k < a.NB) n += a.refs[id + k] == 0;
-    block_scan<kThreads>(n, s, &total);
-    if (threadIdx.x == 0) a.chunk[blockIdx.x] = total;
-    return;
-  }
-  const int i = blockIdx.x - a.chunks;
-  const int now = a.wlen[i], add = a.append[i];
-  const int held = (now + a.bs - 1) / a.bs;
-  const int src = a.fork_src ? a.fork_src[i] : -1;
-  if (src >= 0 && src < a.S) {
-    const int *keep = a.wrows + (int64_t)i * a.W;
-    int32_t *t = a.tables + (int64_t)i * a.W;
-    for (int j = threadIdx.x; j < held; j += kThreads) t[j] = keep[j];
-  }
-  const bool bad = add < 0 || (int64_t)now + add > (int64_t)a.W * a.bs;
-  const int last = write_block(a, i);
-  const int holders = last >= 0 ? a.refs[last] : 0;
-  int before = 0;
-  if (holders > 1)
-    for (int r = threadIdx.x; r < i; r += kThreads) before += write_block(a, r) == last;
-  block_scan<kThreads>(before, s, &total);
-  if (threadIdx.x == 0) {
-    const int cow = holders - total > 1;
-    const int more = bad || add == 0 ? 0 : (int)(((int64_t)now + add + a.bs - 1) / a.bs) - held;
-    if (bad) raise_error(a.err, PA_DEVERR_CONTEXT_LEN);
-    a.info[2 * i] = (more + cow) << 1 | cow;
-    a.info[2 * i + 1] = last;
-  }
-}
-
-// One CTA: prefix sums of the free counts, of the rows' needs and of their
-// tokens; the first row that does not fit ends the growing.
-__global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const StepArgs a) {
-  __shared__ int s[kPlanThreads / 32 + 1];
-  __shared__ int64_t s64[kPlanThreads / 32 + 1];  // sums over rows may pass 32 bits
-  pdl_begin();
-  int avail = 0;
-  for (int c0 = 0; c0 < a.chunks; c0 += kPlanThreads) {
-    const int c = c0 + threadIdx.x;
-    int total;
-    const int n = c < a.chunks ? a.chunk[c] : 0;
-    const int off = block_scan<kPlanThreads>(n, s, &total);
-    if (c < a.chunks) a.chunk[c] = avail + off;
-    avail += total;
-  }
-  int64_t taken = 0, tokens = 0;
-  int best = 0;  // blocks taken by the leading run of rows that fit
-  for (int r0 = 0; r0 < a.S; r0 += kPlanThreads) {
-    const int i = r0 + threadIdx.x;
-    const int add = i < a.S ? max(a.append[i], 0) : 0;
-    const int need = i < a.S ? a.info[2 * i] >> 1 : 0;
-    int64_t t_need, t_add;
-    const int64_t first = taken + block_scan<kPlanThreads, int64_t>(need, s64, &t_need);
-    const int64_t tok = tokens + block_scan<kPlanThreads, int64_t>(add, s64, &t_add);
-    if (i < a.S) {
-      // need is never negative, so the rows that fit are a leading run
-      const bool fits = first + need <= avail;
-      const bool ok = fits && a.append[i] >= 0 && (int64_t)a.wlen[i] + add <= (int64_t)a.W * a.bs;
-      if (!fits && add > 0) raise_error(a.err, PA_DEVERR_POOL);
-      a.base[i] = ok ? (int)first : -1;
-      a.qsl[i] = (int)min(tok, (int64_t)INT_MAX);
-      if (ok) best = max(best, (int)first + need);
-    }
-    taken += t_need;
-    tokens += t_add;
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = best;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kPlanThreads / 32; ++w) best = max(best, s[w]);
-    a.scal[0] = best;
-    a.qsl[a.S] = (int)min(tokens, (int64_t)INT_MAX);
-    if (tokens > a.max_new) raise_error(a.err, PA_DEVERR_SLOT);
-  }
-}
-
-// The free blocks of lowest id, in order, into the list of fresh ones.
-__global__ void __launch_bounds__(kThreads) step_take_kernel(const StepArgs a) {
-  __shared__ int s[kThreads / 32 + 1];
-  pdl_begin();
-  const int take = a.scal[0];
-  int rank = a.chunk[blockIdx.x];
-  if (rank >= take) return;
-  const int id = blockIdx.x * kChunk + threadIdx.x * 4;
-  bool free_[4];
-  int n = 0, total;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    free_[k] = id + k < a.NB && a.refs[id + k] == 0;
-    n += free_[k];
-  }
-  rank += block_scan<kThreads>(n, s, &total);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (free_[k]) {
-      if (rank < take) {
-        a.fresh[rank] = id + k;
-        a.refs[id + k] = 1;
-      }
-      ++rank;
-    }
-}
-
-// One CTA per row: its fresh blocks, slots, length; the CTAs after them fill
-// the rest of slot_mapping.
-__global__ void __launch_bounds__(kThreads) step_apply_kernel(const StepArgs a) {
-  pdl_begin();
-  const int i = blockIdx.x;
-  if (i >= a.S) {
-    const int64_t p = (int64_t)a.qsl[a.S] + (int64_t)(i - a.S) * kThreads + threadIdx.x;
-    for (int64_t x = p; x < a.max_new; x += (int64_t)(gridDim.x - a.S) * kThreads) a.slots[x] = -1;
-    return;
-  }
-  const int now = a.wlen[i], add = max(a.append[i], 0), base = a.base[i];
-  const int info = a.info[2 * i], cow = info & 1, more = (info >> 1) - cow;
-  const int held = (now + a.bs - 1) / a.bs;
-  const int64_t p0 = a.qsl[i];
-  if (base < 0) {
-    if (threadIdx.x == 0) {
-      a.lens[i] = now;
-      a.pairs[2 * i] = a.pairs[2 * i + 1] = -1;
-    }
-    for (int t = threadIdx.x; t < add; t += kThreads)
-      if (p0 + t < a.max_new) a.slots[p0 + t] = -1;
-    return;
-  }
-  int32_t *row = a.tables + (int64_t)i * a.W;
-  for (int k = threadIdx.x; k < more; k += kThreads) row[held + k] = a.fresh[base + cow + k];
-  if (threadIdx.x == 0) {
-    const int last = a.info[2 * i + 1];
-    const int dst = cow ? a.fresh[base] : -1;
-    if (cow) {
-      row[held - 1] = dst;
-      atomicSub(a.refs + last, 1);
-    }
-    a.pairs[2 * i] = cow ? last : -1;
-    a.pairs[2 * i + 1] = dst;
-    a.lens[i] = now + add;
-  }
-  __syncthreads();
-  for (int t = threadIdx.x; t < add; t += kThreads) {
-    if (p0 + t >= a.max_new) break;
-    const int pos = now + t, b = row[pos / a.bs];
-    a.slots[p0 + t] = b >= 0 && b < a.NB ? (int64_t)b * a.bs + pos % a.bs : -1;
-  }
-}
-
-// ---- block moves -----------------------------------------------------------------
-
-// Copies whole blocks (src, dst) in every pool of the list: one 8 KB piece per
-// CTA iteration, four 16-byte loads in flight per thread.  `count`: pairs, on
-// the device; pairs of -1 are skipped.  Bound: memory traffic.
-constexpr int kMoveVecs = 4 * kThreads;
-__global__ void __launch_bounds__(kThreads) move_blocks_kernel(const Pools pools, const int64_t *pairs,
-                                                               const int *count, int max_pairs) {
-  pdl_begin();
-  const int n = count ? min(*count, max_pairs) : max_pairs;
+// Copies whole blocks (src, dst) in every pool of the list: pieces of 4 KB, one
+// a warp, eight 16-byte loads in flight a thread.  Pairs of -1 are skipped.
+// Bound: memory traffic.
+constexpr int kMoveVecs = 8 * 32;
+__device__ __forceinline__ void move_blocks(const Pools &pools, const int64_t *pairs, int n) {
+  const int lane = threadIdx.x & 31;
   for (int k = 0; k < pools.n; ++k) {
     const int64_t vecs = pools.vecs[k];
     const int64_t pieces = (vecs + kMoveVecs - 1) / kMoveVecs;
-    for (int64_t w = blockIdx.x; w < n * pieces; w += gridDim.x) {
-      const int64_t pair = w / pieces, v0 = (w - pair * pieces) * kMoveVecs + threadIdx.x;
+    for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < n * pieces;
+         w += (int64_t)gridDim.x * (kThreads / 32)) {
+      const int64_t pair = w / pieces, v0 = (w - pair * pieces) * kMoveVecs + lane;
+      const int64_t src = pairs[2 * pair], dst = pairs[2 * pair + 1];
+      if (src < 0 || dst < 0) continue;
+      const uint4 *from = pools.p[k] + src * vecs + v0;
+      uint4 *to = pools.p[k] + dst * vecs + v0;
+      const int left = (int)min(vecs - v0, (int64_t)kMoveVecs);
+      uint4 r[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (u * 32 < left) r[u] = __ldcs(from + u * 32);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (u * 32 < left) to[u * 32] = r[u];
+    }
+  }
+}
+
+// The same as a launch of its own, for the pools past the first kPoolsPerLaunch
+// and for moves that a pass of the cooperative grid does not cover: with eight
+// small CTAs a SM and 16 KB pieces it reaches 5.6 TB/s where the cooperative
+// grid's two large ones reach 5.1 (65536 blocks of 32 KB, half of them used).
+constexpr int kMoverThreads = 256, kMoverVecs = 4 * kMoverThreads;
+__global__ void __launch_bounds__(kMoverThreads) move_blocks_kernel(const Pools pools, const int64_t *pairs,
+                                                                    int num_pairs) {
+  for (int k = 0; k < pools.n; ++k) {
+    const int64_t vecs = pools.vecs[k];
+    const int64_t pieces = (vecs + kMoverVecs - 1) / kMoverVecs;
+    for (int64_t w = blockIdx.x; w < num_pairs * pieces; w += gridDim.x) {
+      const int64_t pair = w / pieces, v0 = (w - pair * pieces) * kMoverVecs + threadIdx.x;
       const int64_t src = pairs[2 * pair], dst = pairs[2 * pair + 1];
       if (src < 0 || dst < 0) continue;
       const uint4 *from = pools.p[k] + src * vecs;
@@ -348,12 +182,216 @@ __global__ void __launch_bounds__(kThreads) move_blocks_kernel(const Pools pools
       uint4 r[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (v0 + u * kThreads < vecs) r[u] = __ldcs(from + v0 + u * kThreads);
+        if (v0 + u * kMoverThreads < vecs) r[u] = __ldcs(from + v0 + u * kMoverThreads);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (v0 + u * kThreads < vecs) to[v0 + u * kThreads] = r[u];
+        if (v0 + u * kMoverThreads < vecs) to[v0 + u * kMoverThreads] = r[u];
     }
   }
+}
+
+// ---- pa_table_step ------------------------------------------------------------
+
+__global__ void __launch_bounds__(kThreads, 2) step_kernel(const StepArgs a, const Pools pools) {
+  __shared__ int s[kThreads / 32 + 1];
+  __shared__ int64_t s64[kThreads / 32 + 1];  // sums over rows may pass 32 bits
+  __shared__ int s_group[kRowGroups];
+  cg::grid_group grid = cg::this_grid();
+  const int cap = a.W * a.bs;
+  const int group = threadIdx.x / kRowThreads, gt = threadIdx.x % kRowThreads;
+  const int row0 = blockIdx.x * kRowGroups + group, row_step = gridDim.x * kRowGroups;
+
+  // 1. Rows give up and take over blocks (integer atomics on the counts).  The
+  // blocks of a fork's source are put aside, since its row may itself change.
+  for (int i = row0; i < a.S; i += row_step) {
+    int src = a.fork_src ? a.fork_src[i] : -1;
+    if (src >= a.S) {
+      if (gt == 0) raise_error(a.err, PA_DEVERR_TABLE);
+      src = -1;
+    }
+    const bool forked = src >= 0;
+    const bool drop = forked || (a.release && a.release[i] != 0);
+    const int len = row_len(a.lens, i, cap, gt == 0 ? a.err : nullptr);
+    const int add = a.append[i];
+    const int32_t *own = a.tables + (int64_t)i * a.W, *from = own;
+    int now = drop ? 0 : len;
+    if (drop) {
+      const int n = (len + a.bs - 1) / a.bs;
+      for (int j = gt; j < n; j += kRowThreads) {
+        const int b = own[j];
+        if (b >= 0 && b < a.NB) atomicSub(a.refs + b, 1);
+        else raise_error(a.err, PA_DEVERR_BLOCK_ID);
+      }
+    }
+    if (forked) {
+      now = row_len(a.lens, src, cap, nullptr);
+      from = a.tables + (int64_t)src * a.W;
+      int *keep = a.wrows + (int64_t)i * a.W;
+      const int n = (now + a.bs - 1) / a.bs;
+      for (int j = gt; j < n; j += kRowThreads) {
+        const int b = from[j];
+        keep[j] = b;
+        if (b >= 0 && b < a.NB) atomicAdd(a.refs + b, 1);
+        else raise_error(a.err, PA_DEVERR_BLOCK_ID);
+      }
+    }
+    if (gt == 0) {
+      a.wlen[i] = now;
+      int b = -1;
+      if (add > 0 && now % a.bs != 0 && (int64_t)now + add <= cap) {
+        b = from[now / a.bs];
+        if (b < 0 || b >= a.NB) b = -1;
+      }
+      a.writes[i] = b;
+    }
+  }
+  grid.sync();
+
+  // 2. Free blocks a chunk; forked rows' entries into the tables; the rows'
+  // needs.  Of the rows that write into one shared block, in row order, all copy
+  // it but the last of its holders: the k-th writer of a block with r holders
+  // copies while r - k > 1.
+  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+    const int id = c * kChunk + threadIdx.x * kPerThread;
+    int n = 0, total;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+      if (id + k < a.NB) n += a.refs[id + k] == 0;
+    block_scan(n, s, &total);
+    if (threadIdx.x == 0) a.chunk[c] = total;
+  }
+  for (int i = row0; i < a.S; i += row_step) {
+    const int now = a.wlen[i], add = a.append[i];
+    const int held = (now + a.bs - 1) / a.bs;
+    const int src = a.fork_src ? a.fork_src[i] : -1;
+    if (src >= 0 && src < a.S) {
+      const int *keep = a.wrows + (int64_t)i * a.W;
+      int32_t *t = a.tables + (int64_t)i * a.W;
+      for (int j = gt; j < held; j += kRowThreads) t[j] = keep[j];
+    }
+    const bool bad = add < 0 || (int64_t)now + add > cap;
+    const int last = a.writes[i];
+    const int holders = last >= 0 ? a.refs[last] : 0;
+    int before = 0;
+    if (holders > 1) {  // uniform over the row's threads
+      if (gt == 0) s_group[group] = 0;
+      for (int r = gt; r < i; r += kRowThreads) before += a.writes[r] == last;
+      before = __reduce_add_sync(0xffffffffu, before);
+      named_sync(1 + group, kRowThreads);
+      if ((gt & 31) == 0 && before) atomicAdd(&s_group[group], before);
+      named_sync(1 + group, kRowThreads);
+      before = s_group[group];
+      named_sync(1 + group, kRowThreads);  // read before the next row clears it
+    }
+    if (gt == 0) {
+      const int cow = holders - before > 1;
+      const int more = bad || add == 0 ? 0 : (int)(((int64_t)now + add + a.bs - 1) / a.bs) - held;
+      if (bad) raise_error(a.err, PA_DEVERR_CONTEXT_LEN);
+      a.info[i] = (more + cow) << 1 | cow;
+    }
+  }
+  grid.sync();
+
+  // 3. Every CTA: which rows fit (need is never negative, so they are a leading
+  // run) and how many blocks those take; then the free blocks of lowest id, in
+  // order, into the list of fresh ones.
+  int c0, c1, avail, rank;
+  chunk_range(a.chunks, &c0, &c1);
+  sum_chunks(a.chunk, a.chunks, c0, s, &avail, &rank);
+  int64_t taken = 0, tokens = 0;
+  int take = 0;
+  for (int r0 = 0; r0 < a.S; r0 += kThreads) {
+    const int i = r0 + threadIdx.x;
+    const int add = i < a.S ? a.append[i] : 0;
+    const int need = i < a.S ? a.info[i] >> 1 : 0;
+    int64_t t_need, t_add;
+    const int64_t first = taken + block_scan<int64_t>(need, s64, &t_need);
+    const int64_t tok = tokens + block_scan<int64_t>(max(add, 0), s64, &t_add);
+    const bool fits = first + need <= avail;
+    if (i < a.S) {
+      if (fits) take = max(take, (int)first + need);
+      if (blockIdx.x == 0) {
+        const bool ok = fits && add >= 0 && (int64_t)a.wlen[i] + add <= cap;
+        if (!fits && add > 0) raise_error(a.err, PA_DEVERR_POOL);
+        a.base[i] = ok ? (int)first : -1;
+        a.qsl[i] = (int)min(tok, (int64_t)INT_MAX);
+      }
+    }
+    taken += t_need;
+    tokens += t_add;
+  }
+  take = __reduce_max_sync(0xffffffffu, take);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = take;
+  __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) take = max(take, s[w]);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.qsl[a.S] = (int)min(tokens, (int64_t)INT_MAX);
+    if (tokens > a.max_new) raise_error(a.err, PA_DEVERR_SLOT);
+  }
+  for (int c = c0; c < c1 && rank < take; ++c) {  // CTA-uniform
+    const int id = c * kChunk + threadIdx.x * kPerThread;
+    bool free_[kPerThread];
+    int n = 0, total;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      free_[k] = id + k < a.NB && a.refs[id + k] == 0;
+      n += free_[k];
+    }
+    int x = rank + block_scan(n, s, &total);
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k)
+      if (free_[k]) {
+        if (x < take) {
+          a.fresh[x] = id + k;
+          a.refs[id + k] = 1;
+        }
+        ++x;
+      }
+    rank += total;
+  }
+  grid.sync();
+
+  // 4. The rows' fresh blocks, slots and lengths; -1 behind the last slot.
+  for (int64_t x = (int64_t)a.qsl[a.S] + blockIdx.x * kThreads + threadIdx.x; x < a.max_new;
+       x += (int64_t)gridDim.x * kThreads)
+    a.slots[x] = -1;
+  for (int i = row0; i < a.S; i += row_step) {
+    const int now = a.wlen[i], add = max(a.append[i], 0), base = a.base[i];
+    const int info = a.info[i], cow = info & 1, more = (info >> 1) - cow;
+    const int held = (now + a.bs - 1) / a.bs;
+    const int64_t p0 = a.qsl[i];
+    const bool grown = base >= 0;
+    int32_t *row = a.tables + (int64_t)i * a.W;
+    const int copy = grown && cow ? a.fresh[base] : -1;
+    if (gt == 0) {
+      const int last = a.writes[i];
+      if (copy >= 0) {
+        row[held - 1] = copy;
+        atomicSub(a.refs + last, 1);
+      }
+      a.pairs[2 * i] = copy >= 0 ? last : -1;
+      a.pairs[2 * i + 1] = copy;
+      a.lens[i] = grown ? now + add : now;
+    }
+    if (grown)
+      for (int k = gt; k < more; k += kRowThreads) row[held + k] = a.fresh[base + cow + k];
+    const int n = (int)min((int64_t)add, max((int64_t)0, a.max_new - p0));
+    for (int t = gt; t < n; t += kRowThreads) {
+      const int pos = now + t, j = pos / a.bs;
+      int64_t slot = -1;
+      if (grown) {
+        const int b = j >= held ? a.fresh[base + cow + j - held] : copy >= 0 ? copy : row[j];
+        if (b >= 0 && b < a.NB) slot = (int64_t)b * a.bs + pos % a.bs;
+      }
+      a.slots[p0 + t] = slot;
+    }
+  }
+  if (pools.n == 0) return;  // uniform over the grid
+  grid.sync();
+
+  // 5. Copy-on-write copies in all pools.
+  move_blocks(pools, a.pairs, a.S);
 }
 
 // ---- pa_table_compact ------------------------------------------------------------
@@ -363,118 +401,149 @@ struct CompactArgs {
   const int32_t *lens;
   int64_t *moves;
   int S, W, NB, bs, chunks, max_moves;
-  int *scal, *chunk, *remap, *holes, *sources;
+  int *chunk, *remap, *holes, *sources;
   unsigned int *err;
 };
 
-__global__ void __launch_bounds__(kThreads) compact_count_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) compact_kernel(const CompactArgs a, const Pools pools) {
   __shared__ int s[kThreads / 32 + 1];
-  pdl_begin();
-  const int id = blockIdx.x * kChunk + threadIdx.x * 4;
-  int n = 0, total;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (id + k < a.NB) n += a.refs[id + k] > 0;
-  block_scan<kThreads>(n, s, &total);
-  if (threadIdx.x == 0) a.chunk[blockIdx.x] = total;
-}
+  cg::grid_group grid = cg::this_grid();
 
-// One CTA: used blocks before each chunk, the live count, and the used blocks
-// that already lie below it.
-__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
-  __shared__ int s[kPlanThreads / 32 + 1];
-  pdl_begin();
-  int live = 0, total;
-  for (int c0 = 0; c0 < a.chunks; c0 += kPlanThreads) {
-    const int c = c0 + threadIdx.x;
-    const int n = c < a.chunks ? a.chunk[c] : 0;
-    const int off = block_scan<kPlanThreads>(n, s, &total);
-    if (c < a.chunks) a.chunk[c] = live + off;
-    live += total;
-  }
-  __syncthreads();
-  const int c = live / kChunk;  // the chunk that the border falls into
-  int below = live;
-  if (c < a.chunks) {
-    const int id = c * kChunk + threadIdx.x;
-    block_scan<kPlanThreads, int>(id < live && a.refs[id] > 0, s, &total);
-    below = a.chunk[c] + total;
-  }
-  if (threadIdx.x == 0) {
-    a.scal[0] = live - below;  // moves
-    a.scal[1] = live;
-    a.scal[2] = below;
-    *a.live = live;
-  }
-}
-
-// k-th free id below the border and k-th used id at or past it.
-__global__ void __launch_bounds__(kThreads) compact_list_kernel(const CompactArgs a) {
-  __shared__ int s[kThreads / 32 + 1];
-  pdl_begin();
-  const int live = a.scal[1], below = a.scal[2];
-  const int id = blockIdx.x * kChunk + threadIdx.x * 4;
-  bool used[4];
-  int n = 0, total;
+  // 1. used blocks a chunk
+  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+    const int id = c * kChunk + threadIdx.x * kPerThread;
+    int n = 0, total;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    used[k] = id + k < a.NB && a.refs[id + k] > 0;
-    n += used[k];
+    for (int k = 0; k < kPerThread; ++k)
+      if (id + k < a.NB) n += a.refs[id + k] > 0;
+    block_scan(n, s, &total);
+    if (threadIdx.x == 0) a.chunk[c] = total;
   }
-  int before = a.chunk[blockIdx.x] + block_scan<kThreads>(n, s, &total);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int b = id + k;
-    if (b < live && !used[k]) a.holes[b - before] = b;
-    if (b >= live && b < a.NB) a.remap[b] = b;  // a held block without a count stays where it is
-    if (b >= live && used[k]) a.sources[before - below] = b;
-    before += used[k];
-  }
-}
+  grid.sync();
 
-__global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactArgs a) {
-  pdl_begin();
-  const int n = a.scal[0];
-  const int k = blockIdx.x * kThreads + threadIdx.x;
-  if (k < n) {
-    const int src = a.sources[k], dst = a.holes[k];
-    a.remap[src] = dst;
-    a.refs[dst] = a.refs[src];
-    a.refs[src] = 0;
+  // 2. k-th free id below the border `live` and k-th used id at or past it
+  int c0, c1, live, before, total;
+  chunk_range(a.chunks, &c0, &c1);
+  sum_chunks(a.chunk, a.chunks, c0, s, &live, &before);
+  int below = 0;  // used blocks below the border
+  {
+    const int border = live / kChunk;
+    int x = 0;
+    for (int c = threadIdx.x; c < min(border, a.chunks); c += kThreads) x += a.chunk[c];
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int id = border * kChunk + threadIdx.x * kPerThread + k;
+      if (id < live) x += a.refs[id] > 0;
+    }
+    block_scan(x, s, &below);
+  }
+  const int moves = live - below;
+  for (int c = c0; c < c1; ++c) {
+    const int id = c * kChunk + threadIdx.x * kPerThread;
+    bool used[kPerThread];
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      used[k] = id + k < a.NB && a.refs[id + k] > 0;
+      n += used[k];
+    }
+    int x = before + block_scan(n, s, &total);
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int b = id + k;
+      if (b < live && !used[k]) a.holes[b - x] = b;
+      if (b >= live && b < a.NB) {
+        if (used[k]) a.sources[x - below] = b;
+        else a.remap[b] = b;  // a held block without a count stays where it is
+      }
+      x += used[k];
+    }
+    before += total;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.live = live;
+  grid.sync();
+
+  // 3. the moves
+  for (int k = blockIdx.x * kThreads + threadIdx.x; k < a.max_moves; k += gridDim.x * kThreads) {
+    int src = -1, dst = -1;
+    if (k < moves) {
+      src = a.sources[k];
+      dst = a.holes[k];
+      a.remap[src] = dst;
+      a.refs[dst] = a.refs[src];
+      a.refs[src] = 0;
+    }
     a.moves[2 * (int64_t)k] = src;
     a.moves[2 * (int64_t)k + 1] = dst;
-  } else if (k < a.max_moves) {
-    a.moves[2 * (int64_t)k] = a.moves[2 * (int64_t)k + 1] = -1;
   }
-}
+  grid.sync();
 
-__global__ void __launch_bounds__(kThreads) compact_tables_kernel(const CompactArgs a) {
-  pdl_begin();
-  const int i = blockIdx.x, live = a.scal[1];
-  const int len = row_len(a.lens, i, a.W * a.bs, threadIdx.x == 0 ? a.err : nullptr);
-  int32_t *t = a.tables + (int64_t)i * a.W;
-  const int n = (len + a.bs - 1) / a.bs;
-  for (int j = threadIdx.x; j < n; j += kThreads) {
-    const int b = t[j];
-    if (b < 0 || b >= a.NB) raise_error(a.err, PA_DEVERR_BLOCK_ID);
-    else if (b >= live) t[j] = a.remap[b];
+  // 4. tables, and the blocks of all pools
+  const int group = threadIdx.x / kRowThreads, gt = threadIdx.x % kRowThreads;
+  for (int i = blockIdx.x * kRowGroups + group; i < a.S; i += gridDim.x * kRowGroups) {
+    const int len = row_len(a.lens, i, a.W * a.bs, gt == 0 ? a.err : nullptr);
+    int32_t *t = a.tables + (int64_t)i * a.W;
+    const int n = (len + a.bs - 1) / a.bs;
+    for (int j = gt; j < n; j += kRowThreads) {
+      const int b = t[j];
+      if (b < 0 || b >= a.NB) raise_error(a.err, PA_DEVERR_BLOCK_ID);
+      else if (b >= live) t[j] = a.remap[b];
+    }
   }
+  move_blocks(pools, a.moves, moves);
 }
 
 // ---- host ---------------------------------------------------------------------------
 
+// Cooperative launch: the grid's CTAs are resident together (two a SM at most).
 template <typename... Args>
-cudaError_t launch_dep(void (*kernel)(Args...), int grid, int threads, cudaStream_t stream, Args... args) {
+cudaError_t launch_coop(void (*kernel)(Args...), int grid, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The pools [p0, p0 + kPoolsPerLaunch) of the list, and the CTAs' shares of 16
+// pieces in copying `pairs` blocks of theirs.
+Pools pool_list(void *const *pools, const int64_t *bytes, int n, int p0, int64_t pairs, int64_t *pieces) {
+  Pools list;
+  list.n = n - p0 < kPoolsPerLaunch ? n - p0 : kPoolsPerLaunch;
+  if (list.n < 0) list.n = 0;
+  *pieces = 0;
+  for (int k = 0; k < list.n; ++k) {
+    list.p[k] = static_cast<uint4 *>(pools[p0 + k]);
+    list.vecs[k] = bytes[p0 + k] / 16;
+    const int64_t x = ((list.vecs[k] + kMoveVecs - 1) / kMoveVecs * pairs + kThreads / 32 - 1) / (kThreads / 32);
+    if (x > *pieces) *pieces = x;
+  }
+  return list;
+}
+
+// CTAs: what the largest phase can use, two a SM at most.
+int coop_grid(int64_t want, int sm_count) {
+  const int64_t most = (int64_t)sm_count * 2;
+  return (int)(want < 1 ? 1 : want > most ? most : want);
+}
+
+// Moves in the pools from p0 on, in launches of their own.
+cudaError_t launch_moves(void *const *pools, const int64_t *bytes, int n, int p0, const int64_t *pairs,
+                         int num_pairs, int sm_count, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  for (; p0 < n && e == cudaSuccess; p0 += kPoolsPerLaunch) {
+    int64_t pieces;
+    const Pools list = pool_list(pools, bytes, n, p0, num_pairs, &pieces);
+    const int64_t want = pieces * 4, most = (int64_t)sm_count * 8;  // 16 KB a CTA and pass
+    move_blocks_kernel<<<(unsigned)(want < most ? want : most), kMoverThreads, 0, s>>>(list, pairs, num_pairs);
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 bool pools_ok(void *const *pools, const int64_t *bytes, int n) {
@@ -482,26 +551,6 @@ bool pools_ok(void *const *pools, const int64_t *bytes, int n) {
   for (int i = 0; i < n; ++i)
     if (!pools[i] || (reinterpret_cast<uintptr_t>(pools[i]) & 15u) || bytes[i] <= 0 || bytes[i] % 16) return false;
   return true;
-}
-
-cudaError_t launch_moves(void *const *pools, const int64_t *bytes, int n, const int64_t *pairs,
-                         const int *count, int max_pairs, int sm_count, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  for (int p0 = 0; p0 < n && max_pairs > 0 && e == cudaSuccess; p0 += kPoolsPerLaunch) {
-    Pools list;
-    list.n = n - p0 < kPoolsPerLaunch ? n - p0 : kPoolsPerLaunch;
-    int64_t pieces = 0;
-    for (int k = 0; k < list.n; ++k) {
-      list.p[k] = static_cast<uint4 *>(pools[p0 + k]);
-      list.vecs[k] = bytes[p0 + k] / 16;
-      const int64_t x = (list.vecs[k] + kMoveVecs - 1) / kMoveVecs;
-      if (x > pieces) pieces = x;
-    }
-    int64_t grid = pieces * max_pairs;
-    if (grid > (int64_t)sm_count * 8) grid = (int64_t)sm_count * 8;
-    e = launch_dep(move_blocks_kernel, (int)grid, kThreads, s, list, pairs, count, max_pairs);
-  }
-  return e;
 }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -554,8 +603,8 @@ int pa_table_step(int32_t *block_tables, int max_blocks_per_seq, int32_t *contex
   a.bs = block_size;
   a.max_new = max_new_tokens;
   a.chunks = (num_blocks + kChunk - 1) / kChunk;
-  a.scal = reinterpret_cast<int *>(ws + w.scal);
   a.wlen = reinterpret_cast<int *>(ws + w.len);
+  a.writes = reinterpret_cast<int *>(ws + w.writes);
   a.info = reinterpret_cast<int *>(ws + w.info);
   a.base = reinterpret_cast<int *>(ws + w.base);
   a.chunk = reinterpret_cast<int *>(ws + w.chunk);
@@ -563,15 +612,14 @@ int pa_table_step(int32_t *block_tables, int max_blocks_per_seq, int32_t *contex
   a.wrows = reinterpret_cast<int *>(ws + w.rows);
   a.err = dev.err;
   cudaStream_t s = (cudaStream_t)stream;
-  int tail = (max_new_tokens + kThreads - 1) / kThreads;
-  if (tail > 64) tail = 64;
-  cudaError_t e = launch_dep(step_release_kernel, num_seqs, kThreads, s, (const StepArgs)a);
-  if (e == cudaSuccess) e = launch_dep(step_count_kernel, a.chunks + num_seqs, kThreads, s, (const StepArgs)a);
-  if (e == cudaSuccess) e = launch_dep(step_plan_kernel, 1, kPlanThreads, s, (const StepArgs)a);
-  if (e == cudaSuccess) e = launch_dep(step_take_kernel, a.chunks, kThreads, s, (const StepArgs)a);
-  if (e == cudaSuccess) e = launch_dep(step_apply_kernel, num_seqs + tail, kThreads, s, (const StepArgs)a);
+  int64_t pieces;
+  const Pools list = pool_list(pools, pool_block_bytes, num_pools, 0, num_seqs, &pieces);
+  int64_t want = (num_seqs + kRowGroups - 1) / kRowGroups;
+  if (a.chunks > want) want = a.chunks;
+  if (pieces > want) want = pieces;
+  cudaError_t e = launch_coop(step_kernel, coop_grid(want, dev.sm_count), s, (const StepArgs)a, (const Pools)list);
   if (e == cudaSuccess)
-    e = launch_moves(pools, pool_block_bytes, num_pools, copy_pairs, nullptr, num_seqs, dev.sm_count, s);
+    e = launch_moves(pools, pool_block_bytes, num_pools, kPoolsPerLaunch, copy_pairs, num_seqs, dev.sm_count, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -603,7 +651,6 @@ int pa_table_compact(int32_t *block_tables, int max_blocks_per_seq, const int32_
   a.bs = block_size;
   a.chunks = (num_blocks + kChunk - 1) / kChunk;
   a.max_moves = num_blocks / 2 > 1 ? num_blocks / 2 : 1;
-  a.scal = reinterpret_cast<int *>(ws + w.scal);
   a.chunk = reinterpret_cast<int *>(ws + w.chunk);
   a.remap = reinterpret_cast<int *>(ws + w.list);
   // at most num_blocks / 2 holes are filled, but up to `live` are listed from
@@ -612,14 +659,18 @@ int pa_table_compact(int32_t *block_tables, int max_blocks_per_seq, const int32_
   a.sources = a.holes + num_blocks / 2;
   a.err = dev.err;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = launch_dep(compact_count_kernel, a.chunks, kThreads, s, (const CompactArgs)a);
-  if (e == cudaSuccess) e = launch_dep(compact_plan_kernel, 1, kPlanThreads, s, (const CompactArgs)a);
-  if (e == cudaSuccess) e = launch_dep(compact_list_kernel, a.chunks, kThreads, s, (const CompactArgs)a);
+  int64_t pieces;
+  Pools list = pool_list(pools, pool_block_bytes, num_pools, 0, a.max_moves, &pieces);
+  const bool apart = pieces > dev.sm_count * 2;  // more than a pass of the cooperative grid
+  if (apart) list.n = 0;
+  int64_t want = (num_seqs + kRowGroups - 1) / kRowGroups;
+  if (a.chunks > want) want = a.chunks;
+  if (!apart && pieces > want) want = pieces;
+  cudaError_t e =
+      launch_coop(compact_kernel, coop_grid(want, dev.sm_count), s, (const CompactArgs)a, (const Pools)list);
   if (e == cudaSuccess)
-    e = launch_dep(compact_move_kernel, (a.max_moves + kThreads - 1) / kThreads, kThreads, s, (const CompactArgs)a);
-  if (e == cudaSuccess) e = launch_dep(compact_tables_kernel, num_seqs, kThreads, s, (const CompactArgs)a);
-  if (e == cudaSuccess)
-    e = launch_moves(pools, pool_block_bytes, num_pools, block_moves, a.scal, a.max_moves, dev.sm_count, s);
+    e = launch_moves(pools, pool_block_bytes, num_pools, apart ? 0 : kPoolsPerLaunch, block_moves, a.max_moves,
+                     dev.sm_count, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

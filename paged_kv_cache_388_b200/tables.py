@@ -5,7 +5,9 @@ in device arrays, for loops that must not wait for the host, a captured decode
 loop among them: ``step`` releases, forks and grows all rows in one call and
 hands out the new tokens' slots, copying the blocks that a shared row writes
 into; ``compact`` moves the used blocks to the front of the pool, so that the
-pool's tail can be given back.
+pool's tail can be given back.  Calls on the same tables, captured ones among
+them, must follow one another (one stream, or streams that wait): they update
+the tables and share the object's workspace.
 """
 from __future__ import annotations
 
@@ -34,7 +36,9 @@ class DeviceBlockTables:
         self.context_lens = own(context_lens, (num_seqs,), "context_lens")
         self.ref_counts = own(ref_counts, (num_blocks,), "ref_counts")
         self.device = self.block_tables.device
-        self._ws_bytes = _lib.pa_table_workspace_size(num_seqs, max_blocks_per_seq, num_blocks)
+        # kept with the tables: calls on the same tables follow one another anyway
+        self._ws = torch.empty(_lib.pa_table_workspace_size(num_seqs, max_blocks_per_seq, num_blocks),
+                               dtype=torch.uint8, device=self.device)
 
     @classmethod
     def from_allocator(cls, allocator, sids, max_blocks_per_seq, device="cuda"):
@@ -48,9 +52,6 @@ class DeviceBlockTables:
         return cls(len(sids), max_blocks_per_seq, allocator.num_blocks, allocator.block_size,
                    block_tables=tables.to(device), context_lens=lens.to(device),
                    ref_counts=refs.to(device))
-
-    def _workspace(self):
-        return torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
 
     def step(self, append, max_new_tokens, release=None, fork_src=None, pools=()):
         """One scheduling step: rows with release != 0 give up their blocks,
@@ -67,7 +68,7 @@ class DeviceBlockTables:
         pairs = torch.empty((n, 2), dtype=torch.int64, device=dev)
         _lib.pa_table_step(self.block_tables, self.context_lens, self.ref_counts, append,
                            self.block_size, slots, qsl, pairs, release=release, fork_src=fork_src,
-                           pools=pools, workspace=self._workspace())
+                           pools=pools, workspace=self._ws)
         return slots, qsl, pairs
 
     def compact(self, pools=()):
@@ -78,5 +79,5 @@ class DeviceBlockTables:
         moves = torch.empty((max(1, self.num_blocks // 2), 2), dtype=torch.int64, device=self.device)
         _lib.pa_table_compact(self.block_tables, self.context_lens, self.ref_counts,
                               self.block_size, live, moves, pools=pools,
-                              workspace=self._workspace())
+                              workspace=self._ws)
         return live, moves
