@@ -315,19 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!*abort_flag) raise_error(a.err, PA_DEVERR_TIMEOUT);
     *abort_flag = 1;
   };
-  // a wait of a whole warp; the clock, whose read takes longer than a poll, and
-  // the flag of a failure elsewhere are looked at on every 64th
+  const uint32_t bar0 = smem_addr(bars);
   auto warp_wait = [&](int bar, uint32_t parity) -> bool {
-    bool ok = false;
-    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
-    if (!__all_sync(0xffffffffu, ok)) {
-      const uint64_t t0 = globaltimer_ns();
-      while (!ok && !*abort_flag && globaltimer_ns() - t0 <= kWaitLimitNs)
-        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok && lane == 0) fail();
-    }
-    return ok;
+    return mbar_warp_wait(bar0 + 8 * bar, parity, abort_flag, a.err);
   };
 
   Walk walk(a, line, words[kWStart], words[kWStart + 1], hi - lo, rt);

@@ -11,8 +11,8 @@
 // 128-key tile j and Q tile t the tensor cores compute S_t = Q_t K_j^T (K =
 // DN + 64) and O_t += P_t V_j, fp32 accumulators in tensor memory (128 columns
 // each: all 512 are used); P_t (16 bits, two keys a word) overwrites S_t and
-// is the A operand of P V from there.  The MMA order per tile is PV_0(j),
-// S_0(j+1), PV_1(j), S_1(j+1): the softmax of one Q tile runs under the
+// is the A operand of P V from there.  The chains P V_t(j), S_t(j+1), softmax of
+// the two Q tiles run side by side, so that the softmax of one lies under the
 // products of the other.
 //
 // K and V arrive by TMA in chunks of 128 keys x 64 columns (16 KB, the
@@ -22,7 +22,7 @@
 // flight while tile j is worked on.
 //
 // Warps: 8 softmax (4 per Q tile; thread = row = TMEM lane), 1 TMA producer,
-// 1 MMA issuer that also owns the tensor memory.
+// 2 MMA issuers (one per Q tile; the first also owns the tensor memory).
 #include "latent.h"
 #include "pa_device.cuh"
 #include "tc_common.cuh"
@@ -38,17 +38,17 @@ constexpr int kRing = 8;                   // chunks in flight
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8 between rescales
 constexpr int kSoftmaxWarps = 4 * kQTiles;
 constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kQTiles);
 
 enum {
   kQFull = 0,
   kFull = 1,                    // [kRing] chunk landed
-  kEmpty = kFull + kRing,       // [kRing] products that read the chunk are done
+  kEmpty = kFull + kRing,       // [kRing] both Q tiles' products that read the chunk are done
   kSFull = kEmpty + kRing,      // [Q tile] S in tensor memory
   kPFull = kSFull + kQTiles,    // [Q tile] P written over S (4 warps)
   kPvDone = kPFull + kQTiles,   // [Q tile] P V complete
-  kDone = kPvDone + kQTiles,
-  kNumBars = kDone + 1
+  kDone = kPvDone + kQTiles,    // [Q tile]
+  kNumBars = kDone + kQTiles
 };
 
 template <int DN>
@@ -123,14 +123,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars[kQFull], 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&bars[kFull + s], 1);
-      mbar_init(&bars[kEmpty + s], 1);
+      mbar_init(&bars[kEmpty + s], nq);
     }
     for (int t = 0; t < kQTiles; ++t) {
       mbar_init(&bars[kSFull + t], 1);
       mbar_init(&bars[kPFull + t], 4);
       mbar_init(&bars[kPvDone + t], 1);
+      mbar_init(&bars[kDone + t], 1);
     }
-    mbar_init(&bars[kDone], 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
@@ -151,19 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
   };
 
-  // a wait of a whole warp; the clock, whose read takes longer than a poll, and
-  // the flag of a failure elsewhere are looked at on every 64th
+  const uint32_t bar0 = smem_addr(bars);
   auto warp_wait = [&](int bar, uint32_t parity) -> bool {
-    bool ok = false;
-    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
-    if (!__all_sync(0xffffffffu, ok)) {
-      const uint64_t start = globaltimer_ns();
-      while (!ok && !*abort_flag && globaltimer_ns() - start <= kWaitLimitNs)
-        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(&bars[bar], parity);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok && lane == 0) fail();
-    }
-    return ok;
+    return mbar_warp_wait(bar0 + 8 * bar, parity, abort_flag, a.err);
   };
 
   if (warp == kProducerWarp) {
@@ -196,21 +186,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every copy has landed before the CTA can exit
       if (!mbar_wait(&bars[kQFull], 0) || !drain_ring(&bars[kFull], kRing, issued)) fail();
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ======================= MMA issue ======================================
+    // One warp per Q tile: a thread that has issued products goes on only when
+    // they have started, so one warp for both would hold P_0 V back behind S_1.
     constexpr uint32_t idesc_s = umma_idesc(TT::kFmt, 0, 0, kRows, kKeys);
     constexpr uint32_t idesc_pv = umma_idesc(TT::kFmt, 0, 1, kRows, 64);
     constexpr uint32_t kHi = umma_desc_hi(1024);
-    const uint32_t q_lo = umma_desc_lo(sbase, 16), k_lo = umma_desc_lo(ring, 16), v_lo = umma_desc_lo(ring, kChunk);
-    auto chunk_full = [&](uint32_t x) { return warp_wait(kFull + x % kRing, (x / kRing) & 1); };
+    const int t = warp - kMmaWarp;
+    const int nt = t == nq - 1 ? ntiles : t < nq ? nt0 : 0;
+    const uint32_t a_lo = umma_desc_lo(sbase + t * SH::kQBytes, 16);
+    const uint32_t k_lo = umma_desc_lo(ring, 16), v_lo = umma_desc_lo(ring, kChunk);
+    auto chunks_full = [&](uint32_t x, int n) {
+      bool ok = true;
+      for (int c = 0; c < n && ok; ++c) ok = warp_wait(kFull + (x + c) % kRing, ((x + c) / kRing) & 1);
+      return ok;
+    };
     // S_t(j) = Q_t K_j^T: both K-major, 8-row groups 1 KB apart
-    auto issue_s = [&](int t, int j) -> bool {
+    auto issue_s = [&](int j) -> bool {
       const uint32_t x0 = (uint32_t)j * SH::kTC;
-      for (int c = 0; c < SH::kKC; ++c)
-        if (!chunk_full(x0 + c)) return false;
+      if (!chunks_full(x0, SH::kKC)) return false;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t a_lo = q_lo + t * (SH::kQBytes >> 4), d = tmem + tmem_s_col(t);
+        const uint32_t d = tmem + tmem_s_col(t);
 #pragma unroll
         for (int c = 0; c < SH::kKC; ++c) {
           const uint32_t b_lo = k_lo + ((x0 + c) % kRing) * (kChunk >> 4);
@@ -220,18 +218,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (c | kk) ? 1u : 0u);
         }
         umma_commit(&bars[kSFull + t]);
-        if (t == nq - 1)
-          for (int c = 0; c < SH::kKC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
+        for (int c = 0; c < SH::kKC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
       }
       __syncwarp();
       return true;
     };
     // O_t += P_t(j) V_j: A = P from tensor memory (16 keys in 8 columns), B =
     // V with columns contiguous, 64 of them a product, 8-key groups 1 KB apart
-    auto issue_pv = [&](int t, int j) -> bool {
+    auto issue_pv = [&](int j) -> bool {
       const uint32_t x0 = (uint32_t)j * SH::kTC + SH::kKC;
-      for (int c = 0; c < SH::kVC; ++c)
-        if (!chunk_full(x0 + c)) return false;
+      if (!chunks_full(x0, SH::kVC)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint32_t keep = j > 0 ? 1u : 0u;
@@ -244,31 +240,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                        idesc_pv, ks > 0 ? 1u : keep);
         }
         umma_commit(&bars[kPvDone + t]);
-        if (t == nq - 1)
-          for (int c = 0; c < SH::kVC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
+        for (int c = 0; c < SH::kVC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
       }
       __syncwarp();
       return true;
     };
-    bool ok = warp_wait(kQFull, 0);
-    for (int t = 0; t < nq && ok; ++t)
-      if (t == nq - 1 || nt0 > 0) ok = issue_s(t, 0);
-    for (int j = 0; j < ntiles && ok; ++j) {
+    bool ok = t < nq && warp_wait(kQFull, 0) && (nt == 0 || issue_s(0));
+    for (int j = 0; j < nt && ok; ++j) {
       const uint32_t par = (uint32_t)(j & 1);
-      for (int t = 0; t < nq && ok; ++t) {
-        const int nt = t == nq - 1 ? ntiles : nt0;
-        if (j >= nt) continue;
-        ok = warp_wait(kPFull + t, par);
-        if (!ok) break;
-        tc_fence_after();
-        ok = issue_pv(t, j);
-        // S(j+1) overwrites P(j) of this Q tile: its P V must be complete
-        if (ok && j + 1 < nt) ok = warp_wait(kPvDone + t, par) && issue_s(t, j + 1);
-      }
+      ok = warp_wait(kPFull + t, par) && issue_pv(j);
+      // S(j+1) overwrites P(j): its P V must be complete
+      if (ok && j + 1 < nt) ok = warp_wait(kPvDone + t, par) && issue_s(j + 1);
     }
+    // tiles that only the other Q tile takes: their chunks are let go as they land
+    if (t < nq)
+      for (uint32_t x = (uint32_t)nt * SH::kTC; x < (uint32_t)ntiles * SH::kTC && ok; ++x) {
+        ok = chunks_full(x, 1);
+        if (ok && lane == 0) mbar_arrive(&bars[kEmpty + x % kRing]);
+      }
     if (elect_one()) {
-      umma_commit(&bars[kDone]);  // completes when every MMA above has finished
-      if (!mbar_wait(&bars[kDone], 0)) fail();
+      umma_commit(&bars[kDone + t]);  // completes when every MMA above has finished
+      if (!mbar_wait(&bars[kDone + t], 0)) fail();
     }
     __syncwarp();
   } else {

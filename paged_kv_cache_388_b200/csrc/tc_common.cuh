@@ -141,6 +141,44 @@ __device__ __forceinline__ void umma_ts_lo(uint32_t tmem_d, uint32_t tmem_a, uin
       : "memory");
 }
 
+// Poll a barrier up to 4096 times in a loop of three instructions.  The wait
+// stands in many places of a kernel whose roles share the instruction cache:
+// inlined with its clock and its failure path it took 330 cycles on a barrier
+// that had long completed, this loop 40.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 4096;\n\t"
+      "POLL_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra.uni DONE_%=;\n\t"
+      "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra.uni POLL_%=;\n\t"
+      "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A warp's bounded wait: false after kWaitLimitNs, or at once when another warp
+// has given up (*abort_flag); the first to give up raises PA_DEVERR_TIMEOUT.
+__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                            unsigned int *err) {
+  const uint64_t start = globaltimer_ns();
+  bool ok = false;
+  while (!ok && !*abort_flag && globaltimer_ns() - start <= kWaitLimitNs) ok = mbar_poll(bar, parity);
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok && (threadIdx.x & 31) == 0) {
+    if (!*abort_flag) raise_error(err, PA_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  return ok;
+}
+__device__ __forceinline__ bool mbar_warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                               unsigned int *err) {
+  const bool ok = mbar_poll(bar, parity);
+  return __all_sync(0xffffffffu, ok) || mbar_wait_long(bar, parity, abort_flag, err);
+}
+
 // True in one thread of a converged warp, always the same one.  ptxas keeps
 // what such a thread alone computes in uniform registers, where tcgen05.mma
 // takes its operands from.
