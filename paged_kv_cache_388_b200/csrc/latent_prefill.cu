@@ -34,20 +34,25 @@ constexpr int kRows = 128;  // rows per Q tile (MMA M)
 constexpr int kKeys = 128;  // keys per tile
 constexpr int kQTiles = 2;
 constexpr int kChunk = 128 * 64 * 2;       // bytes of 128 rows x 64 columns
-constexpr int kRing = 8;                   // chunks in flight
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8 between rescales
 constexpr int kSoftmaxWarps = 4 * kQTiles;
 constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kQTiles);
 
+// Barriers of K and V are kept by tile parity: the ring holds two
+// tiles at most, so that a tile's chunks are asked for only after the products of the
+// tile two before have let theirs go.
 enum {
   kQFull = 0,
-  kFull = 1,                    // [kRing] chunk landed
-  kEmpty = kFull + kRing,       // [kRing] both Q tiles' products that read the chunk are done
-  kSFull = kEmpty + kRing,      // [Q tile] S in tensor memory
+  kKFull = 1,                   // [2] K of the tile landed
+  kVFull = kKFull + 2,          // [2] V of the tile landed
+  kKEmpty = kVFull + 2,         // [2] both Q tiles' S done
+  kVEmpty = kKEmpty + 2,        // [2] both Q tiles' P V done
+  kSFull = kVEmpty + 2,         // [Q tile] S in tensor memory
   kPFull = kSFull + kQTiles,    // [Q tile] P written over S (4 warps)
   kPvDone = kPFull + kQTiles,   // [Q tile] P V complete
-  kDone = kPvDone + kQTiles,    // [Q tile]
+  kTurn = kPvDone + kQTiles,    // S_1 of the tile has been issued
+  kDone = kTurn + 1,            // [Q tile]
   kNumBars = kDone + kQTiles
 };
 
@@ -56,6 +61,8 @@ struct Shape {
   static constexpr int kKC = DN / 64 + 1;  // chunks of K a tile
   static constexpr int kVC = DN / 64;      // chunks of V a tile
   static constexpr int kTC = kKC + kVC;
+  // chunks in flight: two tiles at most (see the barriers)
+  static constexpr int kRing = 2 * kTC < 8 ? 2 * kTC : 8;
   static constexpr int kQBytes = kKC * kChunk;  // one Q tile
   static constexpr int kOffRing = kQTiles * kQBytes;
   static constexpr int kOffBar = kOffRing + kRing * kChunk;
@@ -121,9 +128,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- set-up: barriers, tensor memory -------------------------------------
   if (tid == 0) {
     mbar_init(&bars[kQFull], 1);
-    for (int s = 0; s < kRing; ++s) {
-      mbar_init(&bars[kFull + s], 1);
-      mbar_init(&bars[kEmpty + s], nq);
+    mbar_init(&bars[kTurn], 1);
+    for (int p = 0; p < 2; ++p) {
+      mbar_init(&bars[kKFull + p], 1);
+      mbar_init(&bars[kVFull + p], 1);
+      mbar_init(&bars[kKEmpty + p], nq);
+      mbar_init(&bars[kVEmpty + p], nq);
     }
     for (int t = 0; t < kQTiles; ++t) {
       mbar_init(&bars[kSFull + t], 1);
@@ -164,27 +174,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < SH::kKC; ++c)
           tma_load_3d(sbase + t * SH::kQBytes + c * kChunk, &tmq, c * 64, h, q0 + t0 + t * kRows,
                       &bars[kQFull]);
-      uint32_t issued = 0;
-      bool ok = true;
-      for (int j = 0; j < ntiles && ok; ++j) {
+    }
+    __syncwarp();
+    uint32_t x = 0;              // chunk
+    int last_k = -1, last_v = -1;  // last tile whose K (V) was announced
+    bool ok = true;
+    for (int j = 0; j < ntiles && ok; ++j) {
+      const int row = k0 + j * kKeys, p = j & 1;
 #pragma unroll
-        for (int c = 0; c < SH::kTC; ++c) {
-          const uint32_t slot = issued % kRing;
-          ok = !*abort_flag && mbar_wait(&bars[kEmpty + slot], ((issued / kRing) & 1) ^ 1);
+      for (int c = 0; c < SH::kTC; ++c, ++x) {
+        if (x >= SH::kRing) {  // the chunk SH::kRing before has been let go with its tile's K or V
+          const uint32_t tj = (x - SH::kRing) / SH::kTC, tc = (x - SH::kRing) % SH::kTC;
+          ok = warp_wait((tc < SH::kKC ? kKEmpty : kVEmpty) + (tj & 1), (tj >> 1) & 1);
           if (!ok) break;
-          const uint32_t dst = ring + slot * kChunk;
-          uint64_t *bar = &bars[kFull + slot];
-          mbar_arrive_expect_tx(bar, kChunk);
-          const int row = k0 + j * kKeys;
+        }
+        if (lane == 0) {
+          const uint32_t dst = ring + (x % SH::kRing) * kChunk;
+          uint64_t *bar = &bars[(c < SH::kKC ? kKFull : kVFull) + p];
+          if (c == 0) mbar_arrive_expect_tx(bar, SH::kKC * kChunk);
+          if (c == SH::kKC) mbar_arrive_expect_tx(bar, SH::kVC * kChunk);
           if (c < SH::kKC - 1) tma_load_3d(dst, &tmk, c * 64, h, row, bar);
           else if (c == SH::kKC - 1) tma_load_2d(dst, &tmr, 0, row, bar);
           else tma_load_3d(dst, &tmv, (c - SH::kKC) * 64, h, row, bar);
-          ++issued;
         }
+        __syncwarp();
+        if (c == SH::kKC - 1) last_k = j;
+        if (c == SH::kTC - 1) last_v = j;
       }
-      if (!ok) fail();
-      // every copy has landed before the CTA can exit
-      if (!mbar_wait(&bars[kQFull], 0) || !drain_ring(&bars[kFull], kRing, issued)) fail();
+    }
+    // Every copy has landed before the CTA can exit.  After a failure part of a
+    // tile's chunks may be on their way under a barrier that waits for the
+    // others too: what is missing is taken off it.
+    if (!ok && lane == 0) {
+      const int j = (int)(x / SH::kTC), c = (int)(x % SH::kTC);
+      if (c > 0 && c < SH::kKC) mbar_complete_tx(&bars[kKFull + (j & 1)], (SH::kKC - c) * kChunk), last_k = j;
+      if (c > SH::kKC) mbar_complete_tx(&bars[kVFull + (j & 1)], (SH::kTC - c) * kChunk), last_v = j;
+    }
+    if (lane == 0) {
+      bool landed = mbar_wait(&bars[kQFull], 0);
+      for (int j = last_k; j >= 0 && j > last_k - 2; --j) landed = mbar_wait(&bars[kKFull + (j & 1)], (j >> 1) & 1) && landed;
+      for (int j = last_v; j >= 0 && j > last_v - 2; --j) landed = mbar_wait(&bars[kVFull + (j & 1)], (j >> 1) & 1) && landed;
+      if (!landed) fail();
     }
   } else if (warp >= kMmaWarp) {
     // ======================= MMA issue ======================================
@@ -197,66 +227,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nt = t == nq - 1 ? ntiles : t < nq ? nt0 : 0;
     const uint32_t a_lo = umma_desc_lo(sbase + t * SH::kQBytes, 16);
     const uint32_t k_lo = umma_desc_lo(ring, 16), v_lo = umma_desc_lo(ring, kChunk);
-    auto chunks_full = [&](uint32_t x, int n) {
-      bool ok = true;
-      for (int c = 0; c < n && ok; ++c) ok = warp_wait(kFull + (x + c) % kRing, ((x + c) / kRing) & 1);
-      return ok;
-    };
     // S_t(j) = Q_t K_j^T: both K-major, 8-row groups 1 KB apart
-    auto issue_s = [&](int j) -> bool {
+    auto issue_s = [&](int j) {
       const uint32_t x0 = (uint32_t)j * SH::kTC;
-      if (!chunks_full(x0, SH::kKC)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint32_t d = tmem + tmem_s_col(t);
 #pragma unroll
         for (int c = 0; c < SH::kKC; ++c) {
-          const uint32_t b_lo = k_lo + ((x0 + c) % kRing) * (kChunk >> 4);
+          const uint32_t b_lo = k_lo + ((x0 + c) % SH::kRing) * (kChunk >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_lo(d, a_lo + ((c * kChunk + kk * 32) >> 4), kHi, b_lo + ((kk * 32) >> 4), kHi, idesc_s,
                     (c | kk) ? 1u : 0u);
         }
         umma_commit(&bars[kSFull + t]);
-        for (int c = 0; c < SH::kKC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
+        umma_commit(&bars[kKEmpty + (j & 1)]);
+        if (t == 1) mbar_arrive(&bars[kTurn]);
       }
       __syncwarp();
-      return true;
     };
     // O_t += P_t(j) V_j: A = P from tensor memory (16 keys in 8 columns), B =
     // V with columns contiguous, 64 of them a product, 8-key groups 1 KB apart
-    auto issue_pv = [&](int j) -> bool {
+    auto issue_pv = [&](int j) {
       const uint32_t x0 = (uint32_t)j * SH::kTC + SH::kKC;
-      if (!chunks_full(x0, SH::kVC)) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint32_t keep = j > 0 ? 1u : 0u;
 #pragma unroll
         for (int c = 0; c < SH::kVC; ++c) {
-          const uint32_t b_lo = v_lo + ((x0 + c) % kRing) * (kChunk >> 4);
+          const uint32_t b_lo = v_lo + ((x0 + c) % SH::kRing) * (kChunk >> 4);
 #pragma unroll
           for (int ks = 0; ks < kKeys / 16; ++ks)
             umma_ts_lo(tmem + tmem_o_col(t) + c * 64, tmem + tmem_s_col(t) + ks * 8, b_lo + ((ks * 2048) >> 4), kHi,
                        idesc_pv, ks > 0 ? 1u : keep);
         }
         umma_commit(&bars[kPvDone + t]);
-        for (int c = 0; c < SH::kVC; ++c) umma_commit(&bars[kEmpty + (x0 + c) % kRing]);
+        umma_commit(&bars[kVEmpty + (j & 1)]);
       }
       __syncwarp();
-      return true;
     };
-    bool ok = t < nq && warp_wait(kQFull, 0) && (nt == 0 || issue_s(0));
-    for (int j = 0; j < nt && ok; ++j) {
-      const uint32_t par = (uint32_t)(j & 1);
-      ok = warp_wait(kPFull + t, par) && issue_pv(j);
-      // S(j+1) overwrites P(j): its P V must be complete
-      if (ok && j + 1 < nt) ok = warp_wait(kPvDone + t, par) && issue_s(j + 1);
+    // The two chains are kept half a step apart: S_1(j) is issued when P_0(j) is
+    // there, S_0(j+1) when S_1(j) has been issued.  In step they would meet at
+    // the exponentials (16 a cycle and SM: 1024 cycles for a tile of 128 x 128),
+    // then leave those units idle together.
+    const bool pair = nq == 2;
+    auto s_turn = [&](int j) -> bool {
+      bool ok = warp_wait(kKFull + (j & 1), (j >> 1) & 1);
+      if (pair && t == 1 && j < nt0) ok = ok && warp_wait(kPFull + 0, j & 1);
+      if (pair && t == 0 && j > 0) ok = ok && warp_wait(kTurn, (j - 1) & 1);
+      return ok;
+    };
+    bool ok = t < nq && warp_wait(kQFull, 0);
+    if (ok && nt > 0) {
+      ok = s_turn(0);
+      if (ok) issue_s(0);
     }
-    // tiles that only the other Q tile takes: their chunks are let go as they land
+    for (int j = 0; j < nt && ok; ++j) {
+      ok = warp_wait(kVFull + (j & 1), (j >> 1) & 1) && warp_wait(kPFull + t, j & 1);
+      if (!ok) break;
+      issue_pv(j);
+      if (j + 1 == nt) break;
+      // S(j+1) overwrites P(j): its P V must be complete
+      ok = s_turn(j + 1) && warp_wait(kPvDone + t, j & 1);
+      if (ok) issue_s(j + 1);
+    }
+    // tiles that only the other Q tile takes are let go as they land
     if (t < nq)
-      for (uint32_t x = (uint32_t)nt * SH::kTC; x < (uint32_t)ntiles * SH::kTC && ok; ++x) {
-        ok = chunks_full(x, 1);
-        if (ok && lane == 0) mbar_arrive(&bars[kEmpty + x % kRing]);
+      for (int j = nt; j < ntiles && ok; ++j) {
+        ok = warp_wait(kKFull + (j & 1), (j >> 1) & 1);
+        if (ok && lane == 0) mbar_arrive(&bars[kKEmpty + (j & 1)]);
+        ok = ok && warp_wait(kVFull + (j & 1), (j >> 1) & 1);
+        if (ok && lane == 0) mbar_arrive(&bars[kVEmpty + (j & 1)]);
       }
     if (elect_one()) {
       umma_commit(&bars[kDone + t]);  // completes when every MMA above has finished
@@ -348,11 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys past the last one, in the sequence's last tile: zero their V rows
         // (P is 0 there, but 0 * NaN is not).  The warps of the first Q tile that
         // takes the tile do it before its P V.
-        if ((j + 1) * kKeys > L && (qt == 0 || j >= nt0)) {
+        if ((j + 1) * kKeys > L && (qt == 0 || j >= nt0) && warp_wait(kVFull + (j & 1), (j >> 1) & 1)) {
           for (int c = 0; c < SH::kVC; ++c) {
             const uint32_t x = (uint32_t)j * SH::kTC + SH::kKC + c;
-            if (!mbar_wait(&bars[kFull + x % kRing], (x / kRing) & 1)) { fail(); break; }
-            const uint32_t vst = ring + (x % kRing) * kChunk;
+            const uint32_t vst = ring + (x % SH::kRing) * kChunk;
             for (int i = (L - j * kKeys) * 8 + r; i < kKeys * 8; i += kRows) st_shared_v4(vst + i * 16, 0, 0, 0, 0);
           }
           fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
