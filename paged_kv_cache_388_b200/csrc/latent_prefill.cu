@@ -49,9 +49,9 @@ enum {
   kKEmpty = kVFull + 2,         // [2] both Q tiles' S done
   kVEmpty = kKEmpty + 2,        // [2] both Q tiles' P V done
   kSFull = kVEmpty + 2,         // [Q tile] S in tensor memory
-  kPFull = kSFull + kQTiles,    // [Q tile] P written over S (4 warps)
-  kPvDone = kPFull + kQTiles,   // [Q tile] P V complete
-  kTurn = kPvDone + kQTiles,    // S_1 of the tile has been issued
+  kPFull = kSFull + kQTiles,    // [Q tile][half] 64 keys of P written over S (4 warps)
+  kPvDone = kPFull + 2 * kQTiles,  // [Q tile] P V complete
+  kTurn = kPvDone + kQTiles,    // S_1 of the tile is being issued
   kDone = kTurn + 1,            // [Q tile]
   kNumBars = kDone + kQTiles
 };
@@ -72,6 +72,14 @@ static_assert(Shape<128>::kSmem <= 227 * 1024, "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t tmem_s_col(int t) { return (uint32_t)t * 256u; }
 __device__ __forceinline__ uint32_t tmem_o_col(int t) { return (uint32_t)t * 256u + 128u; }
+
+// Scores of keys past the last visible one (`last`, counted from the first of
+// these 64 columns) become -infinity.
+__device__ __forceinline__ void mask_keys(uint32_t (&s)[2][32], int last) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (i > last) s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
+}
 
 template <typename T, int DN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -137,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < kQTiles; ++t) {
       mbar_init(&bars[kSFull + t], 1);
-      mbar_init(&bars[kPFull + t], 4);
+      mbar_init(&bars[kPFull + 2 * t], 4);
+      mbar_init(&bars[kPFull + 2 * t + 1], 4);
       mbar_init(&bars[kPvDone + t], 1);
       mbar_init(&bars[kDone + t], 1);
     }
@@ -233,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (elect_one()) {
         const uint32_t d = tmem + tmem_s_col(t);
+        if (t == 1) mbar_arrive(&bars[kTurn]);
 #pragma unroll
         for (int c = 0; c < SH::kKC; ++c) {
           const uint32_t b_lo = k_lo + ((x0 + c) % SH::kRing) * (kChunk >> 4);
@@ -243,38 +253,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(&bars[kSFull + t]);
         umma_commit(&bars[kKEmpty + (j & 1)]);
-        if (t == 1) mbar_arrive(&bars[kTurn]);
       }
       __syncwarp();
     };
     // O_t += P_t(j) V_j: A = P from tensor memory (16 keys in 8 columns), B =
     // V with columns contiguous, 64 of them a product, 8-key groups 1 KB apart
-    auto issue_pv = [&](int j) {
+    auto issue_pv = [&](int j, int half) {
       const uint32_t x0 = (uint32_t)j * SH::kTC + SH::kKC;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t keep = j > 0 ? 1u : 0u;
+        const uint32_t keep = (j | half) ? 1u : 0u;
+        const uint32_t pcol = tmem + tmem_s_col(t) + half * 32;
 #pragma unroll
         for (int c = 0; c < SH::kVC; ++c) {
-          const uint32_t b_lo = v_lo + ((x0 + c) % SH::kRing) * (kChunk >> 4);
+          const uint32_t b_lo = v_lo + ((x0 + c) % SH::kRing) * (kChunk >> 4) + half * (8192 >> 4);
 #pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
-            umma_ts_lo(tmem + tmem_o_col(t) + c * 64, tmem + tmem_s_col(t) + ks * 8, b_lo + ((ks * 2048) >> 4), kHi,
-                       idesc_pv, ks > 0 ? 1u : keep);
+          for (int ks = 0; ks < kKeys / 32; ++ks)
+            umma_ts_lo(tmem + tmem_o_col(t) + c * 64, pcol + ks * 8, b_lo + ((ks * 2048) >> 4), kHi, idesc_pv,
+                       ks > 0 ? 1u : keep);
         }
-        umma_commit(&bars[kPvDone + t]);
-        umma_commit(&bars[kVEmpty + (j & 1)]);
+        if (half) {
+          umma_commit(&bars[kPvDone + t]);
+          umma_commit(&bars[kVEmpty + (j & 1)]);
+        }
       }
       __syncwarp();
     };
-    // The two chains are kept half a step apart: S_1(j) is issued when P_0(j) is
-    // there, S_0(j+1) when S_1(j) has been issued.  In step they would meet at
+    // The two chains are kept half a step apart: S_1(j) is issued when half of
+    // P_0(j) is there, S_0(j+1) when S_1(j) has been issued.  In step they would meet at
     // the exponentials (16 a cycle and SM: 1024 cycles for a tile of 128 x 128),
     // then leave those units idle together.
     const bool pair = nq == 2;
     auto s_turn = [&](int j) -> bool {
       bool ok = warp_wait(kKFull + (j & 1), (j >> 1) & 1);
-      if (pair && t == 1 && j < nt0) ok = ok && warp_wait(kPFull + 0, j & 1);
+      if (pair && t == 1 && j < nt0) ok = ok && warp_wait(kPFull, j & 1);
       if (pair && t == 0 && j > 0) ok = ok && warp_wait(kTurn, (j - 1) & 1);
       return ok;
     };
@@ -284,9 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) issue_s(0);
     }
     for (int j = 0; j < nt && ok; ++j) {
-      ok = warp_wait(kVFull + (j & 1), (j >> 1) & 1) && warp_wait(kPFull + t, j & 1);
+      ok = warp_wait(kVFull + (j & 1), (j >> 1) & 1) && warp_wait(kPFull + 2 * t, j & 1);
+      if (ok) issue_pv(j, 0);
+      ok = ok && warp_wait(kPFull + 2 * t + 1, j & 1);
       if (!ok) break;
-      issue_pv(j);
+      issue_pv(j, 1);
       if (j + 1 == nt) break;
       // S(j+1) overwrites P(j): its P V must be complete
       ok = s_turn(j + 1) && warp_wait(kPvDone + t, j & 1);
@@ -324,25 +338,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(kSFull + qt, (uint32_t)(j & 1));
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
-        tmem_wait_ld();
+        // Two passes over S, 64 columns at a time in rolled loops: unrolled, with S
+        // kept in registers between them, the loop overflows the instruction
+        // cache that the softmax and MMA warps of a quarter of the SM share.
         const int kt = j * kKeys;
-        if (kt + kKeys - 1 > limit_lo) {
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if (kt + i > limit) s[i >> 5][i & 31] = __float_as_uint(-INFINITY);
-        }
-        float mx4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx4[c] = -INFINITY;
+        const bool masked = kt + kKeys - 1 > limit_lo;  // warp-uniform
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t s[2][32];
+          tmem_ld32(ts + 64 * hf, s[0]);
+          tmem_ld32(ts + 64 * hf + 32, s[1]);
+          tmem_wait_ld();
+          if (masked) mask_keys(s, limit - kt - 64 * hf);
+          float m2[2] = {mx, mx};
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
-            mx4[c] = fmax3(mx4[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) m2[c] = fmax3(m2[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+          mx = fmaxf(m2[0], m2[1]);
         }
-        float mx = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]);
         mx *= sl2;
         // lazy rescale: move the reference only when the tile's maximum exceeds
         // it by more than 2^8 (first tile with a visible key: always).  O_t is
@@ -365,28 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16(to + 16 * c, o);
           }
         }
-        // P = 2^(s * scale * log2 e - m), key pairs in packed arithmetic; the sum
-        // takes the unrounded weights (lse keeps fp32 accuracy), the product P
-        // rounded to 16 bits: an error of half a step a weight, of the size of
-        // the result's own rounding
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float2 sl2x2 = make_float2(sl2, sl2), negx2 = make_float2(-ref, -ref);
-        float2 psum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = make_float2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1]));
-            const float2 e = __ffma2_rn(x, sl2x2, negx2);
-            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            psum = __fadd2_rn(psum, p);
-            w[i] = TT::pack(p.x, p.y);
-          }
-          tmem_st16(ts + 16 * c, w);
-        }
-        l += psum.x + psum.y;
-        tmem_wait_st();
         // keys past the last one, in the sequence's last tile: zero their V rows
         // (P is 0 there, but 0 * NaN is not).  The warps of the first Q tile that
         // takes the tile do it before its P V.
@@ -398,9 +391,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
         }
-        tc_fence_before();  // the tcgen05.st of P -> the MMA thread
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kPFull + qt]);
+        // P = 2^(s * scale * log2 e - m), key pairs in packed arithmetic; the sum
+        // takes the unrounded weights (lse keeps fp32 accuracy), the product P
+        // rounded to 16 bits: an error of half a step a weight, of the size of
+        // the result's own rounding
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 sl2x2 = make_float2(sl2, sl2), negx2 = make_float2(-ref, -ref);
+        float2 psum = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t s[2][32];
+          tmem_ld32(ts + 64 * hf, s[0]);
+          tmem_ld32(ts + 64 * hf + 32, s[1]);
+          tmem_wait_ld();
+          if (masked) mask_keys(s, limit - kt - 64 * hf);
+          uint32_t w[2][16];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 x = make_float2(__uint_as_float(s[i >> 4][2 * (i & 15)]),
+                                         __uint_as_float(s[i >> 4][2 * (i & 15) + 1]));
+            const float2 e = __ffma2_rn(x, sl2x2, negx2);
+            const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            psum = __fadd2_rn(psum, p);
+            w[i >> 4][i & 15] = TT::pack(p.x, p.y);
+          }
+          // over columns already read: keys 64 hf .. go to columns 32 hf ..
+          tmem_st16(ts + 32 * hf, w[0]);
+          tmem_st16(ts + 32 * hf + 16, w[1]);
+          tmem_wait_st();
+          tc_fence_before();  // the stores of P (and O) -> the MMA thread
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kPFull + 2 * qt + hf]);  // half of P for the product
+        }
+        l += psum.x + psum.y;
       }
       // ---- epilogue: O / l -> out ----
       const bool fin = ok && !*abort_flag && (nt == 0 || warp_wait(kPvDone + qt, (uint32_t)((nt - 1) & 1)));
