@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_sync(1, 128);
       const volatile float *inv = row_inv + (item & 1) * 64;
       constexpr int kC = SH::kMTiles * NR;  // columns of O^T: 128 values a row, tile after tile
-      constexpr int kW = kC < 64 ? kC : 64;  // read at once
+      constexpr int kW = 32;  // read at once
 #pragma unroll 1
       for (int c0 = 0; c0 < kC; c0 += kW) {
         uint32_t o[kW / 16][16];

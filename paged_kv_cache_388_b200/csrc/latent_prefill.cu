@@ -283,27 +283,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // P_0(j) is there, S_0(j+1) when S_1(j) has been issued.  In step they would meet at
     // the exponentials (16 a cycle and SM: 1024 cycles for a tile of 128 x 128),
     // then leave those units idle together.
+    // The waits that are usually over go before those that are not.
     const bool pair = nq == 2;
-    auto s_turn = [&](int j) -> bool {
-      bool ok = warp_wait(kKFull + (j & 1), (j >> 1) & 1);
-      if (pair && t == 1 && j < nt0) ok = ok && warp_wait(kPFull, j & 1);
-      if (pair && t == 0 && j > 0) ok = ok && warp_wait(kTurn, (j - 1) & 1);
-      return ok;
+    auto k_ready = [&](int j) { return warp_wait(kKFull + (j & 1), (j >> 1) & 1); };
+    auto turn = [&](int j) {
+      if (pair && t == 1 && j < nt0) return warp_wait(kPFull, j & 1);
+      if (pair && t == 0 && j > 0) return warp_wait(kTurn, (j - 1) & 1);
+      return true;
     };
     bool ok = t < nq && warp_wait(kQFull, 0);
     if (ok && nt > 0) {
-      ok = s_turn(0);
+      ok = k_ready(0) && turn(0);
       if (ok) issue_s(0);
     }
     for (int j = 0; j < nt && ok; ++j) {
+      const bool more = j + 1 < nt;
       ok = warp_wait(kVFull + (j & 1), (j >> 1) & 1) && warp_wait(kPFull + 2 * t, j & 1);
       if (ok) issue_pv(j, 0);
+      if (more) ok = ok && k_ready(j + 1) && (t == 1 || turn(j + 1));
       ok = ok && warp_wait(kPFull + 2 * t + 1, j & 1);
       if (!ok) break;
       issue_pv(j, 1);
-      if (j + 1 == nt) break;
+      if (!more) break;
       // S(j+1) overwrites P(j): its P V must be complete
-      ok = s_turn(j + 1) && warp_wait(kPvDone + t, j & 1);
+      ok = warp_wait(kPvDone + t, j & 1) && (t == 0 || turn(j + 1));
       if (ok) issue_s(j + 1);
     }
     // tiles that only the other Q tile takes are let go as they land
@@ -338,27 +341,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(kSFull + qt, (uint32_t)(j & 1));
         if (!ok) break;
         tc_fence_after();
-        // Two passes over S, 64 columns at a time in rolled loops: unrolled, with S
-        // kept in registers between them, the loop overflows the instruction
-        // cache that the softmax and MMA warps of a quarter of the SM share.
+        // Two passes over S, 64 columns at a time.  The first ends with the columns
+        // that the second begins with; the others are read again under its work.
+        // (All 128 kept in registers spill at the 168 that 11 warps leave.)
         const int kt = j * kKeys;
         const bool masked = kt + kKeys - 1 > limit_lo;  // warp-uniform
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t s[2][32];
-          tmem_ld32(ts + 64 * hf, s[0]);
-          tmem_ld32(ts + 64 * hf + 32, s[1]);
-          tmem_wait_ld();
-          if (masked) mask_keys(s, limit - kt - 64 * hf);
-          float m2[2] = {mx, mx};
+        float m2[2] = {-INFINITY, -INFINITY};
+        uint32_t s0[2][32], s1[2][32];
+        tmem_ld32(ts + 64, s1[0]);
+        tmem_ld32(ts + 96, s1[1]);
+        tmem_wait_ld();
+        tmem_ld32(ts, s0[0]);
+        tmem_ld32(ts + 32, s0[1]);
+        if (masked) mask_keys(s1, limit - kt - 64);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
+        for (int i = 0; i < 32; i += 2)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) m2[c] = fmax3(m2[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-          mx = fmaxf(m2[0], m2[1]);
-        }
-        mx *= sl2;
+          for (int c = 0; c < 2; ++c) m2[c] = fmax3(m2[c], __uint_as_float(s1[c][i]), __uint_as_float(s1[c][i + 1]));
+        tmem_wait_ld();
+        if (masked) mask_keys(s0, limit - kt);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) m2[c] = fmax3(m2[c], __uint_as_float(s0[c][i]), __uint_as_float(s0[c][i + 1]));
+        const float mx = fmaxf(m2[0], m2[1]) * sl2;
         // lazy rescale: move the reference only when the tile's maximum exceeds
         // it by more than 2^8 (first tile with a visible key: always).  O_t is
         // at rest here: S_t(j) was issued after P V of tile j-1 completed.
@@ -398,13 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 sl2x2 = make_float2(sl2, sl2), negx2 = make_float2(-ref, -ref);
         float2 psum = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t s[2][32];
-          tmem_ld32(ts + 64 * hf, s[0]);
-          tmem_ld32(ts + 64 * hf + 32, s[1]);
-          tmem_wait_ld();
-          if (masked) mask_keys(s, limit - kt - 64 * hf);
+        auto weigh = [&](uint32_t (&s)[2][32], int hf) {
           uint32_t w[2][16];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -422,7 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();  // the stores of P (and O) -> the MMA thread
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kPFull + 2 * qt + hf]);  // half of P for the product
-        }
+        };
+        tmem_ld32(ts + 64, s1[0]);
+        tmem_ld32(ts + 96, s1[1]);
+        weigh(s0, 0);
+        tmem_wait_ld();
+        if (masked) mask_keys(s1, limit - kt - 64);
+        weigh(s1, 1);
         l += psum.x + psum.y;
       }
       // ---- epilogue: O / l -> out ----
