@@ -50,10 +50,6 @@ constexpr int kThreads = 224;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kBadSlots = 16;  // more than the items the producer can be ahead by
 constexpr int kMaxStages = 6;
-// What an item costs beside its tiles (its queries, its epilogue), in tiles:
-// with it the ranges of a batch of short and long sequences end together.
-constexpr int kItemTiles = 2;
-
 // KT keys a tile
 template <int R, int NR, int KT>
 struct Shape {
@@ -113,18 +109,19 @@ struct Seq {
   int tiles, L, q0, Q;
 };
 
-// How the work is laid out in a line of units.  Lockstep: a sequence has
-// kItemTiles + tiles units and each worker is `lanes` CTAs, one per row tile,
+// How the work is laid out in a line of units: an item (a sequence's tiles for
+// one row tile) has one unit a tile and `extra` for what it costs beside them.
+// Lockstep: a sequence is one item and each worker is `lanes` CTAs, one per row tile,
 // that read the same keys at the same time (one of them from memory).  Flat
-// (lanes 1): a sequence has that many units per row tile it really has, and a
-// worker is one CTA; for batches whose sequences differ in rows.
+// (lanes 1): a sequence is an item per row tile it really has, and a worker is
+// one CTA; for batches whose sequences differ in rows.
 struct Line {
-  int workers, lanes, flat, nr, kt;
+  int workers, lanes, flat, nr, kt, extra;
   __device__ __forceinline__ int row_tiles(const Seq &x, int heads) const {
     return flat ? (x.Q * heads + nr - 1) / nr : 1;
   }
   __device__ __forceinline__ int units(const Seq &x, int heads) const {
-    return x.tiles ? (x.tiles + kItemTiles) * row_tiles(x, heads) : 0;
+    return x.tiles ? (x.tiles + extra) * row_tiles(x, heads) : 0;
   }
 };
 
@@ -187,14 +184,14 @@ struct Walk {
         off = 0;
         continue;
       }
-      const int per = x.tiles + kItemTiles;
+      const int per = x.tiles + ln.extra;
       const int rt = ln.flat ? off / per : 0;
       const int at = off - rt * per;
       const int take = min(left, per - at);
       off += take;
       left -= take;
-      t0 = max(0, at - kItemTiles);
-      t1 = max(0, at + take - kItemTiles);
+      t0 = max(0, at - ln.extra);
+      t1 = max(0, at + take - ln.extra);
       first_row = (rt + lane_rt) * ln.nr;
       if (t1 > t0 && first_row < x.Q * a.num_heads) return true;
     }
@@ -694,7 +691,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     if (row >= rows) break;  // a whole warp, and only where no barrier follows
     const int rt = row / line.nr, r = row % line.nr;
     // units of the row's tiles, and the workers that hold them
-    const int u0 = p0 + kItemTiles + (line.flat ? rt * (x.tiles + kItemTiles) : 0);
+    const int u0 = p0 + line.extra + (line.flat ? rt * (x.tiles + line.extra) : 0);
     const int w0 = x.tiles ? owner(u0) : 0, w1 = x.tiles ? owner(u0 + x.tiles - 1) : 0;
     const int np = x.tiles ? w1 - w0 + 1 : 0;
     if (np == 1) continue;  // written by its worker (uniform where barriers follow: one row a CTA)
@@ -807,6 +804,10 @@ Plan plan_of(int num_seqs, int max_query_len, int num_heads, int latent_dim, int
   p.line.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   p.line.kt = key_tile(latent_dim);
   p.row_tiles = (int)((rows + p.line.nr - 1) / p.line.nr);
+  // An item's queries and epilogue, in tiles: CTAs with one item and with four
+  // or five of 256 ragged sequences then end within a few microseconds (2.6 us
+  // an item at 16 rows, 8 at 64 of 512 values, beside 0.8 a tile).
+  p.line.extra = 3 + p.line.nr * latent_dim / 8192;
   p.line.flat = ragged && p.row_tiles > 1;
   p.line.lanes = p.line.flat ? 1 : p.row_tiles;
   p.line.workers = sm_count / p.line.lanes;
@@ -901,7 +902,7 @@ size_t latent_decode_ws(int num_seqs, int max_query_len, int num_heads, int late
 
 bool latent_decode_fits(int num_seqs, int max_query_len, int num_heads, int latent_dim, int max_context_len) {
   const Plan p = plan_of(num_seqs, max_query_len, num_heads, latent_dim, 1, 1);
-  const int64_t per = (int64_t)(max_context_len / p.line.kt + 1 + kItemTiles) * p.row_tiles;
+  const int64_t per = (int64_t)(max_context_len / p.line.kt + 1 + p.line.extra) * p.row_tiles;
   return per <= INT_MAX / num_seqs && (int64_t)num_seqs * max_query_len * num_heads <= INT_MAX;
 }
 
