@@ -657,10 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the records of the sequences that were cut, writes zeros where there
-// is no key to see.  One CTA per (sequence, rows_per_cta rows): 8 rows, a warp
-// each, when there are rows enough to fill the machine, else one row whose
-// pieces the 8 warps share and join through shared memory (one long sequence
-// is cut into as many pieces as there are workers).
+// is no key to see.  One CTA of 8 warps per (sequence, rows_per_cta rows): a
+// warp a row when there are rows enough to fill the machine, else 2, 4 or 8
+// warps that share a row's pieces and join through shared memory (one long
+// sequence is cut into as many pieces as there are workers).
 constexpr int kMergeWarps = 8;
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * kMergeWarps)
@@ -684,17 +684,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
                   : (int)((((int64_t)u + 1) * workers - 1) / total);
   };
   if (x.tiles && owner(p0) == owner(p0 + line.units(x, a.num_heads) - 1)) return;  // written by its worker
-  const bool shared_row = rows_per_cta == 1;
-  const int step = shared_row ? kMergeWarps : 1;
+  const int share = kMergeWarps / rows_per_cta, group = warp / share, part = warp % share;
   for (int base = (int)(blockIdx.x % per_seq) * rows_per_cta; base < rows; base += per_seq * rows_per_cta) {
-    const int row = base + (shared_row ? 0 : warp);
-    if (row >= rows) break;  // a whole warp, and only where no barrier follows
+    const int row = base + group;  // the same for all warps that meet at the barrier below
+    if (row >= rows) break;
     const int rt = row / line.nr, r = row % line.nr;
     // units of the row's tiles, and the workers that hold them
     const int u0 = p0 + line.extra + (line.flat ? rt * (x.tiles + line.extra) : 0);
     const int w0 = x.tiles ? owner(u0) : 0, w1 = x.tiles ? owner(u0 + x.tiles - 1) : 0;
     const int np = x.tiles ? w1 - w0 + 1 : 0;
-    if (np == 1) continue;  // written by its worker (uniform where barriers follow: one row a CTA)
+    if (np == 1) continue;  // written by its worker
     // record of the i-th piece: the first starts the sequence, the others continue it
     auto at = [&](int i) {
       return (((int64_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * line.lanes + (line.flat ? 0 : rt)) * line.nr + r;
@@ -705,12 +704,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, l = 0.f;
     bool bad = false;
-    for (int i0 = shared_row ? warp : 0; i0 < np; i0 += 4 * step) {
+    for (int i0 = part; i0 < np; i0 += 4 * share) {
       float2 ml[4];
       float4 p[4][V];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * step;
+        const int i = i0 + u * share;
         ml[u] = make_float2(-INFINITY, 0.f);
         if (i >= np) continue;
         const int64_t k = at(i);
@@ -740,21 +739,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         }
       }
     }
-    if (shared_row) {  // one row a CTA: the barriers are uniform
-      __syncthreads();
+    if (share > 1) {
+      named_sync(1 + group, 32 * share);  // an earlier row has been joined
 #pragma unroll
       for (int v = 0; v < V; ++v) so[warp][v * 32 + lane] = o[v];
       if (lane == 0) {
         sm[warp] = M;
         sl[warp] = bad ? -1.f : l;
       }
-      __syncthreads();
-      if (warp) continue;
-      for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, sm[w]);
+      named_sync(1 + group, 32 * share);
+      if (part) continue;
+      for (int w = warp; w < warp + share; ++w) M = fmaxf(M, sm[w]);
       l = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < kMergeWarps; ++w) {
+      for (int w = warp; w < warp + share; ++w) {
         bad = bad || sl[w] < 0.f;
         if (sm[w] == -INFINITY && sl[w] <= 0.f) continue;
         const float f = exp2f(sm[w] - M);
@@ -870,7 +869,8 @@ cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, kern, a, tmq, tmc, rec, ml, pref, p.line);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.max_query_len * a.num_heads;
-  const int rows_per_cta = a.num_seqs * rows >= 4096 ? kMergeWarps : 1;
+  int rows_per_cta = 1;  // 512 CTAs at most, if a warp a row allows it
+  while (rows_per_cta < kMergeWarps && a.num_seqs * rows > 512 * (int64_t)rows_per_cta) rows_per_cta *= 2;
   cfg.gridDim = dim3((unsigned)(a.num_seqs * ((rows + rows_per_cta - 1) / rows_per_cta)));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
