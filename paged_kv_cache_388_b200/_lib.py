@@ -482,26 +482,24 @@ def _dev_rows(t, name, dtype, cur):
                          "call under torch.cuda.device(...) of the tensors' device")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, strides = t.shape, list(t.stride())
-    packed = 1
-    for i in range(len(shape) - 1, -1, -1):
-        if shape[i] <= 1:
-            strides[i] = packed
-        packed *= max(shape[i], 1)
+    shape, strides = t.shape, t.stride()
+    if 0 in shape or 1 in shape:
+        strides, packed = list(strides), 1
+        for i in range(len(shape) - 1, -1, -1):
+            if shape[i] <= 1:
+                strides[i] = packed
+            packed *= max(shape[i], 1)
     if strides[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    for st in strides[:-1]:
-        if st % 8:
-            raise ValueError(f"rows of {name} must start on 16-byte boundaries")
-    if t.data_ptr() % 16:
+    if t.data_ptr() % 16 or strides[0] % 8 or strides[-2] % 8:  # two or three dimensions
         raise ValueError(f"rows of {name} must start on 16-byte boundaries")
     return strides[:-1]
 
 
 def _latent_shape(latent_cache):
     """(num_blocks, block_size, row width) of a latent cache."""
-    _shape(latent_cache.dim() == 3,
-           "latent_cache must be [num_blocks, block_size, latent_dim + rope_dim]")
+    if not (latent_cache.dim() == 3):
+        raise ValueError("latent_cache must be [num_blocks, block_size, latent_dim + rope_dim]")
     return tuple(latent_cache.shape)
 
 
@@ -509,12 +507,12 @@ def pa_latent_write(latent, rope, latent_cache, slot_mapping, stream=None):
     """latent [T, R] and rope [T, Dr] (rows may be strided slices); latent_cache
     [NB, bs, R + Dr]; slot_mapping int64 [T], negative slots are skipped."""
     nb, bs, w = _latent_shape(latent_cache)
-    _shape(latent.dim() == 2 and rope.dim() == 2 and latent.shape[0] == rope.shape[0],
-           "latent and rope must hold one row per token")
-    _shape(latent.shape[1] + rope.shape[1] == w,
-           f"latent and rope rows must add up to the cache's {w} values")
-    _shape(slot_mapping.dim() == 1 and slot_mapping.shape[0] == latent.shape[0],
-           "slot_mapping must hold one slot per token")
+    if not (latent.dim() == 2 and rope.dim() == 2 and latent.shape[0] == rope.shape[0]):
+        raise ValueError("latent and rope must hold one row per token")
+    if not (latent.shape[1] + rope.shape[1] == w):
+        raise ValueError(f"latent and rope rows must add up to the cache's {w} values")
+    if not (slot_mapping.dim() == 1 and slot_mapping.shape[0] == latent.shape[0]):
+        raise ValueError("slot_mapping must hold one slot per token")
     cur = _here(latent_cache, "latent_cache")
     _dev(latent_cache, "latent_cache", None, cur)
     ls, = _dev_rows(latent, "latent", latent_cache.dtype, cur)
@@ -538,21 +536,25 @@ def pa_latent_decode(out, lse, q, latent_cache, block_tables, context_lens, scal
     int32 [S]; query_start_loc int32 [S + 1] or None; workspace: uint8 CUDA
     tensor of >= pa_latent_decode_workspace_size(...) bytes."""
     nb, bs, w = _latent_shape(latent_cache)
-    _shape(q.dim() == 3 and q.shape[2] == w, f"q must be [tokens, heads, {w}] to match the cache")
+    if not (q.dim() == 3 and q.shape[2] == w):
+        raise ValueError(f"q must be [tokens, heads, {w}] to match the cache")
     tq, h, _ = q.shape
-    _shape(out.dim() == 3 and tuple(out.shape[:2]) == (tq, h) and out.shape[2] < w,
-           "out must be [tokens, heads, latent_dim]")
+    if not (out.dim() == 3 and tuple(out.shape[:2]) == (tq, h) and out.shape[2] < w):
+        raise ValueError("out must be [tokens, heads, latent_dim]")
     r = out.shape[2]
-    _shape(lse is None or tuple(lse.shape) == (tq, h), "lse must be [tokens, heads]")
-    _shape(block_tables.dim() == 2, "block_tables must be [num_seqs, max_blocks_per_seq]")
+    if not (lse is None or tuple(lse.shape) == (tq, h)):
+        raise ValueError("lse must be [tokens, heads]")
+    if not (block_tables.dim() == 2):
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
     s, mbps = block_tables.shape
-    _shape(context_lens.dim() == 1 and context_lens.shape[0] == s,
-           "block_tables and context_lens disagree on the number of sequences")
+    if not (context_lens.dim() == 1 and context_lens.shape[0] == s):
+        raise ValueError("block_tables and context_lens disagree on the number of sequences")
     if query_start_loc is None:
-        _shape(tq == s, "without query_start_loc q must hold one row per sequence")
+        if not (tq == s):
+            raise ValueError("without query_start_loc q must hold one row per sequence")
     else:
-        _shape(query_start_loc.dim() == 1 and query_start_loc.shape[0] == s + 1,
-               "query_start_loc must have num_seqs + 1 entries")
+        if not (query_start_loc.dim() == 1 and query_start_loc.shape[0] == s + 1):
+            raise ValueError("query_start_loc must have num_seqs + 1 entries")
     cur = _here(q, "q")
     if query_start_loc is not None:
         _dev(query_start_loc, "query_start_loc", torch.int32, cur)
@@ -579,19 +581,23 @@ def pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_
     """out [Tq, H, Dv]; lse float32 [Tq, H] or None; q [Tq, H, Dn + Dr]; k
     [Tk, H, Dn], v [Tk, H, Dv] and k_rope [Tk, Dr] (tokens and heads may be
     strided); query_start_loc and context_start_loc int32 [S + 1]."""
-    _shape(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and k_rope.dim() == 2,
-           "q, k and v must be [tokens, heads, dim], k_rope [tokens, dim]")
+    if not (q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and k_rope.dim() == 2):
+        raise ValueError("q, k and v must be [tokens, heads, dim], k_rope [tokens, dim]")
     tq, h, dq = q.shape
     tk, _, dn = k.shape
     dr, dv = k_rope.shape[1], v.shape[2]
-    _shape(dn + dr == dq, "q rows must hold nope_dim + rope_dim values")
-    _shape(k.shape[1] == h and tuple(v.shape[:2]) == (tk, h) and k_rope.shape[0] == tk,
-           "k, v and k_rope must hold the same tokens, k and v q's heads")
-    _shape(tuple(out.shape) == (tq, h, dv), "out must be [tokens, heads, v_dim]")
-    _shape(lse is None or tuple(lse.shape) == (tq, h), "lse must be [tokens, heads]")
-    _shape(query_start_loc.dim() == 1 and query_start_loc.shape[0] >= 1 and
-           query_start_loc.shape == context_start_loc.shape,
-           "query_start_loc and context_start_loc must have num_seqs + 1 entries each")
+    if not (dn + dr == dq):
+        raise ValueError("q rows must hold nope_dim + rope_dim values")
+    if not (k.shape[1] == h and tuple(v.shape[:2]) == (tk, h) and k_rope.shape[0] == tk):
+        raise ValueError("k, v and k_rope must hold the same tokens, k and v q's heads")
+    if not (tuple(out.shape) == (tq, h, dv)):
+        raise ValueError("out must be [tokens, heads, v_dim]")
+    if not (lse is None or tuple(lse.shape) == (tq, h)):
+        raise ValueError("lse must be [tokens, heads]")
+    if not (query_start_loc.dim() == 1 and
+            query_start_loc.shape[0] >= 1 and
+            query_start_loc.shape == context_start_loc.shape):
+        raise ValueError("query_start_loc and context_start_loc must have num_seqs + 1 entries each")
     cur = _here(q, "q")
     _dev(q, "q", None, cur)
     _dev(out, "out", q.dtype, cur)
@@ -611,10 +617,12 @@ def pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_
 
 
 def _table_shapes(block_tables, context_lens, ref_counts):
-    _shape(block_tables.dim() == 2, "block_tables must be [num_seqs, max_blocks_per_seq]")
-    _shape(tuple(context_lens.shape) == (block_tables.shape[0],),
-           "block_tables and context_lens disagree on the number of sequences")
-    _shape(ref_counts.dim() == 1, "ref_counts must be [num_blocks]")
+    if not (block_tables.dim() == 2):
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    if not (tuple(context_lens.shape) == (block_tables.shape[0],)):
+        raise ValueError("block_tables and context_lens disagree on the number of sequences")
+    if not (ref_counts.dim() == 1):
+        raise ValueError("ref_counts must be [num_blocks]")
     cur = _here(block_tables, "block_tables")
     _dev(block_tables, "block_tables", torch.int32, cur)
     _dev(context_lens, "context_lens", torch.int32, cur)
@@ -630,8 +638,8 @@ def _pool_args(pools, num_blocks, cur):
     ptrs, sizes = (P * n)(), (L * n)()
     for i, t in enumerate(pools):
         _dev(t, "pool", None, cur)
-        _shape(t.dim() >= 1 and t.shape[0] == num_blocks,
-               f"a pool must hold {num_blocks} blocks, got {tuple(t.shape)}")
+        if not (t.dim() >= 1 and t.shape[0] == num_blocks):
+            raise ValueError(f"a pool must hold {num_blocks} blocks, got {tuple(t.shape)}")
         ptrs[i] = t.data_ptr()
         sizes[i] = t.stride(0) * t.element_size() if num_blocks > 1 else t.numel() * t.element_size()
     return ptrs, sizes, n
@@ -651,12 +659,15 @@ def pa_table_step(block_tables, context_lens, ref_counts, append, block_size, sl
     s, w, nb, cur = _table_shapes(block_tables, context_lens, ref_counts)
     for name, t in (("append", append), ("release", release), ("fork_src", fork_src)):
         if t is not None:
-            _shape(tuple(t.shape) == (s,), f"{name} must hold one entry per sequence")
+            if not (tuple(t.shape) == (s,)):
+                raise ValueError(f"{name} must hold one entry per sequence")
             _dev(t, name, torch.int32, cur)
-    _shape(slot_mapping.dim() == 1, "slot_mapping must be [max_new_tokens]")
-    _shape(tuple(query_start_loc.shape) == (s + 1,),
-           "query_start_loc must have num_seqs + 1 entries")
-    _shape(tuple(copy_pairs.shape) == (s, 2), "copy_pairs must be [num_seqs, 2]")
+    if not (slot_mapping.dim() == 1):
+        raise ValueError("slot_mapping must be [max_new_tokens]")
+    if not (tuple(query_start_loc.shape) == (s + 1,)):
+        raise ValueError("query_start_loc must have num_seqs + 1 entries")
+    if not (tuple(copy_pairs.shape) == (s, 2)):
+        raise ValueError("copy_pairs must be [num_seqs, 2]")
     _dev(slot_mapping, "slot_mapping", torch.int64, cur)
     _dev(query_start_loc, "query_start_loc", torch.int32, cur)
     _dev(copy_pairs, "copy_pairs", torch.int64, cur)
@@ -678,9 +689,10 @@ def pa_table_compact(block_tables, context_lens, ref_counts, block_size, num_liv
     pools' blocks are updated in place; num_live int32 [1] and block_moves
     int64 [max(1, NB // 2), 2] are written."""
     s, w, nb, cur = _table_shapes(block_tables, context_lens, ref_counts)
-    _shape(tuple(num_live.shape) == (1,), "num_live must be [1]")
-    _shape(tuple(block_moves.shape) == (max(1, nb // 2), 2),
-           "block_moves must be [max(1, num_blocks // 2), 2]")
+    if not (tuple(num_live.shape) == (1,)):
+        raise ValueError("num_live must be [1]")
+    if not (tuple(block_moves.shape) == (max(1, nb // 2), 2)):
+        raise ValueError("block_moves must be [max(1, num_blocks // 2), 2]")
     _dev(num_live, "num_live", torch.int32, cur)
     _dev(block_moves, "block_moves", torch.int64, cur)
     ptrs, sizes, n = _pool_args(pools, nb, cur)

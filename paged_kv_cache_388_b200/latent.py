@@ -32,6 +32,7 @@ class PagedLatentCache:
         self.num_blocks, self.block_size = num_blocks, block_size
         self.latent_dim, self.rope_dim = latent_dim, rope_dim
         self.dtype, self.device = latent_cache.dtype, latent_cache.device
+        self._ws_bytes = {}  # by batch sizes
 
     def write(self, latent, rope, slot_mapping):
         """Store rows latent [T, latent_dim] | rope [T, rope_dim] in their slots
@@ -47,13 +48,15 @@ class PagedLatentCache:
         (float32 [Tq, H]) receives the logarithm of the softmax sums, by which
         partial results over disjoint keys are merged."""
         if out is None:
-            out = torch.empty((*q.shape[:-1], self.latent_dim), dtype=q.dtype, device=q.device)
+            out = q.new_empty((*q.shape[:-1], self.latent_dim))
         elif out.shape[-1] != self.latent_dim:
             raise ValueError(f"out must be [tokens, heads, {self.latent_dim}]")
         rows = 1 if query_start_loc is None else min(max_query_len, q.shape[0])
-        need = _lib.pa_latent_decode_workspace_size(block_tables.shape[0], rows, q.shape[1],
-                                                    self.latent_dim)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        sizes = (block_tables.shape[0], rows, q.shape[1], self.latent_dim)
+        need = self._ws_bytes.get(sizes)
+        if need is None:
+            need = self._ws_bytes[sizes] = _lib.pa_latent_decode_workspace_size(*sizes)
+        ws = q.new_empty(need, dtype=torch.uint8)
         _lib.pa_latent_decode(out, lse, q, self.latent_cache, block_tables, context_lens, scale,
                               query_start_loc=query_start_loc, max_query_len=max_query_len,
                               max_context_len=max_context_len, workspace=ws)
@@ -67,7 +70,7 @@ def latent_prefill(q, k, k_rope, v, query_start_loc, context_start_loc, scale, m
     with Q rows and L keys sees keys 0 .. L-Q+t, or all L with causal=False.
     Returns out [Tq, H, Dv]; rows past the last sequence are left unwritten."""
     if out is None:
-        out = torch.empty((*q.shape[:-1], v.shape[-1]), dtype=q.dtype, device=q.device)
+        out = q.new_empty((*q.shape[:-1], v.shape[-1]))
     _lib.pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_loc, scale,
                            max_query_len, causal=causal)
     return out

@@ -62,10 +62,10 @@ class DeviceBlockTables:
         int64 [num_seqs, 2]; the copies are done in all ``pools`` ([num_blocks,
         ...] tensors).  When the pool runs out the row and all later growing
         ones stay as they are (PA_DEVERR_POOL in the device error word)."""
-        n, dev = self.num_seqs, self.device
-        slots = torch.empty(max_new_tokens, dtype=torch.int64, device=dev)
-        qsl = torch.empty(n + 1, dtype=torch.int32, device=dev)
-        pairs = torch.empty((n, 2), dtype=torch.int64, device=dev)
+        n, t = self.num_seqs, self.block_tables
+        slots = t.new_empty(max_new_tokens, dtype=torch.int64)
+        qsl = t.new_empty(n + 1)
+        pairs = t.new_empty((n, 2), dtype=torch.int64)
         _lib.pa_table_step(self.block_tables, self.context_lens, self.ref_counts, append,
                            self.block_size, slots, qsl, pairs, release=release, fork_src=fork_src,
                            pools=pools, workspace=self._ws)
@@ -75,8 +75,8 @@ class DeviceBlockTables:
         """Move the used blocks to ids [0, live) in the tables and in all
         ``pools``.  Returns live (int32 [1]) and the moves (src, dst), int64
         [max(1, num_blocks // 2), 2] filled up with (-1, -1)."""
-        live = torch.empty(1, dtype=torch.int32, device=self.device)
-        moves = torch.empty((max(1, self.num_blocks // 2), 2), dtype=torch.int64, device=self.device)
+        live = self.block_tables.new_empty(1)
+        moves = self.block_tables.new_empty((max(1, self.num_blocks // 2), 2), dtype=torch.int64)
         _lib.pa_table_compact(self.block_tables, self.context_lens, self.ref_counts,
                               self.block_size, live, moves, pools=pools,
                               workspace=self._ws)
