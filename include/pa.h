@@ -582,6 +582,8 @@ size_t pa_latent_decode_workspace_size(int num_seqs, int max_query_len,
  *   query_start_loc, context_start_loc  int32 [num_seqs + 1]: a sequence's
  *            rows of q and its rows of k, k_rope and v
  *   max_query_len  host bound of any sequence's Q
+ *   workspace      >= pa_latent_prefill_workspace_size(...) bytes, 16-byte
+ *                  aligned; one each for calls whose kernels may overlap
  * Base pointers and strides are multiples of 16 bytes.  Supported: nope_dim =
  * v_dim in {64, 128}, rope_dim 64, PA_F16 and PA_BF16, scale finite and >= 0.
  * Device checks: offsets out of range or more than max_query_len rows set
@@ -597,8 +599,14 @@ int pa_latent_prefill(void *out, float *lse, const void *q, const void *k,
                       const int32_t *context_start_loc, int num_seqs,
                       int num_q_tokens, int num_k_tokens, int max_query_len,
                       int num_heads, int nope_dim, int rope_dim, int v_dim,
-                      float scale, int causal, int dtype,
-                      struct CUstream_st *stream);
+                      float scale, int causal, int dtype, void *workspace,
+                      size_t workspace_bytes, struct CUstream_st *stream);
+
+/* Workspace bytes pa_latent_prefill needs (current device); 0 where no item is
+ * split over the keys. */
+size_t pa_latent_prefill_workspace_size(int num_seqs, int num_q_tokens,
+                                        int num_k_tokens, int num_heads,
+                                        int nope_dim);
 
 /*
  * ---- Block tables on the device -------------------------------------------

@@ -68,7 +68,9 @@ _lib.pa_latent_decode_workspace_size.restype = SZ
 _lib.pa_latent_decode_workspace_size.argtypes = [I, I, I, I]
 _lib.pa_latent_prefill.restype = I
 _lib.pa_latent_prefill.argtypes = [P, P, P, P, P, P, L, L, L, L, L, P, P, I, I, I, I, I, I, I, I, F,
-                                   I, I, P]
+                                   I, I, P, SZ, P]
+_lib.pa_latent_prefill_workspace_size.restype = SZ
+_lib.pa_latent_prefill_workspace_size.argtypes = [I, I, I, I, I]
 _lib.pa_table_step.restype = I
 _lib.pa_table_step.argtypes = [P, I, P, P, P, P, P, I, I, I, P, I, P, P, P, P, I, P, SZ, P]
 _lib.pa_table_compact.restype = I
@@ -576,11 +578,18 @@ def pa_latent_decode(out, lse, q, latent_cache, block_tables, context_lens, scal
     _check(rc, "pa_latent_decode")
 
 
+def pa_latent_prefill_workspace_size(num_seqs, num_q_tokens, num_k_tokens, num_heads,
+                                     nope_dim) -> int:
+    return int(_lib.pa_latent_prefill_workspace_size(num_seqs, num_q_tokens, num_k_tokens, num_heads,
+                                                     nope_dim))
+
+
 def pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_loc, scale,
-                      max_query_len, causal=True, stream=None):
+                      max_query_len, causal=True, workspace=None, stream=None):
     """out [Tq, H, Dv]; lse float32 [Tq, H] or None; q [Tq, H, Dn + Dr]; k
     [Tk, H, Dn], v [Tk, H, Dv] and k_rope [Tk, Dr] (tokens and heads may be
-    strided); query_start_loc and context_start_loc int32 [S + 1]."""
+    strided); query_start_loc and context_start_loc int32 [S + 1]; workspace:
+    uint8 CUDA tensor of >= pa_latent_prefill_workspace_size(...) bytes."""
     if not (q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and k_rope.dim() == 2):
         raise ValueError("q, k and v must be [tokens, heads, dim], k_rope [tokens, dim]")
     tq, h, dq = q.shape
@@ -608,11 +617,15 @@ def pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_
         _dev(lse, "lse", torch.float32, cur)
     _dev(query_start_loc, "query_start_loc", torch.int32, cur)
     _dev(context_start_loc, "context_start_loc", torch.int32, cur)
+    if workspace is not None:
+        _dev(workspace, "workspace", None, cur)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = _lib.pa_latent_prefill(_ptr(out), _ptr(lse), _ptr(q), _ptr(k), _ptr(k_rope), _ptr(v),
                                 ks, kh, krs, vs, vh, _ptr(query_start_loc),
                                 _ptr(context_start_loc), query_start_loc.shape[0] - 1, tq, tk,
                                 int(max_query_len), h, dn, dr, dv, float(scale),
-                                1 if causal else 0, _DT.get(q.dtype, -1), _stream(stream))
+                                1 if causal else 0, _DT.get(q.dtype, -1), _ptr(workspace),
+                                ws_bytes, _stream(stream))
     _check(rc, "pa_latent_prefill")
 
 

@@ -157,13 +157,21 @@ int pa_latent_decode(void *out, float *lse, const void *q, const void *latent_ca
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+size_t pa_latent_prefill_workspace_size(int num_seqs, int num_q_tokens, int num_k_tokens, int num_heads,
+                                        int nope_dim) {
+  if (num_seqs <= 0 || num_q_tokens <= 0 || num_k_tokens <= 0 || num_heads <= 0 || nope_dim <= 0) return 0;
+  DevInfo dev;
+  if (device_info(&dev) != cudaSuccess) return 0;
+  return latent_prefill_ws(num_seqs, num_q_tokens, num_k_tokens, num_heads, nope_dim, dev.sm_count);
+}
+
 int pa_latent_prefill(void *out, float *lse, const void *q, const void *k, const void *k_rope,
                       const void *v, int64_t k_token_stride, int64_t k_head_stride,
                       int64_t k_rope_stride, int64_t v_token_stride, int64_t v_head_stride,
                       const int32_t *query_start_loc, const int32_t *context_start_loc, int num_seqs,
                       int num_q_tokens, int num_k_tokens, int max_query_len, int num_heads,
                       int nope_dim, int rope_dim, int v_dim, float scale, int causal, int dtype,
-                      struct CUstream_st *stream) {
+                      void *workspace, size_t workspace_bytes, struct CUstream_st *stream) {
   if (num_seqs < 0 || num_q_tokens < 0 || num_k_tokens < 0 || num_heads <= 0 || max_query_len < 1 ||
       !scale_ok(scale))
     return PA_ERR_INVALID_ARG;
@@ -181,7 +189,10 @@ int pa_latent_prefill(void *out, float *lse, const void *q, const void *k, const
   if (max_query_len > num_q_tokens) max_query_len = num_q_tokens;
   DevInfo dev;
   if (device_info(&dev) != cudaSuccess) return PA_ERR_CUDA;
+  const size_t need = latent_prefill_ws(num_seqs, num_q_tokens, num_k_tokens, num_heads, nope_dim, dev.sm_count);
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PA_ERR_WORKSPACE;
   LatentPrefillArgs a{};
+  a.ws = workspace;
   a.out = out;
   a.lse = lse;
   a.q = q;

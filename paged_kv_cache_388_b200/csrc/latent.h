@@ -35,8 +35,10 @@ struct LatentPrefillArgs {
   const int32_t *query_start_loc, *context_start_loc;
   int num_seqs, num_q_tokens, num_k_tokens, max_query_len, num_heads, nope_dim, causal;
   float scale_log2;
+  void *ws;
   unsigned int *err;
 };
+size_t latent_prefill_ws(int num_seqs, int num_q_tokens, int num_k_tokens, int num_heads, int nope_dim, int sm_count);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int dtype, int sm_count, cudaStream_t stream);
 
 }  // namespace pa

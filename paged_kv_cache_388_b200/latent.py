@@ -71,6 +71,9 @@ def latent_prefill(q, k, k_rope, v, query_start_loc, context_start_loc, scale, m
     Returns out [Tq, H, Dv]; rows past the last sequence are left unwritten."""
     if out is None:
         out = q.new_empty((*q.shape[:-1], v.shape[-1]))
+    need = _lib.pa_latent_prefill_workspace_size(query_start_loc.shape[0] - 1, q.shape[0], k.shape[0],
+                                                 q.shape[1], v.shape[-1])
+    ws = q.new_empty(need, dtype=torch.uint8) if need else None
     _lib.pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_loc, scale,
-                           max_query_len, causal=causal)
+                           max_query_len, causal=causal, workspace=ws)
     return out

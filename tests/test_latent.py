@@ -319,6 +319,46 @@ def test_prefill_not_causal(lib, dn):
     _check_prefill(lib, [200, 5, 3, 64], [150, 0, 700, 128], 2, dn, "f16", causal=False, pad_rows=2)
 
 
+@pytest.mark.parametrize("qs,ks,heads,causal", [
+    ([100], [5000], 4, True),  # a few rows over a long prefix: their keys are split over the machine
+    ([1], [9001], 1, True), ([130, 1, 17], [1500, 1, 3000], 2, True), ([300], [700], 3, True), ([257], [4096], 1, False),
+    ([700, 0, 5], [1100, 0, 0], 1, True), ([1500], [1100], 1, True), ([40, 900], [3000, 130], 5, True)])
+@pytest.mark.parametrize("dn", [128, 64])
+def test_prefill_split_over_the_keys(lib, dn, qs, ks, heads, causal):
+    _check_prefill(lib, qs, ks, heads, dn, "bf16", causal=causal, seed=heads, pad_rows=3)
+
+
+def test_workspaces_may_hold_anything(lib):
+    """Bytes that read as NaN in the workspace, and one byte too few."""
+    g = torch.Generator().manual_seed(2)
+    cache, tables = _paged([3000, 70, 1], 16, 576, torch.bfloat16, 0)
+    args = (_randn(g, 3, 16, 576).to(torch.bfloat16).cuda(), cache.cuda(), tables.cuda(),
+            torch.tensor([3000, 70, 1], dtype=torch.int32).cuda(), 0.05)
+    need = lib.pa_latent_decode_workspace_size(3, 1, 16, 512)
+    outs = []
+    for fill in (0, 255):
+        outs.append(torch.empty(3, 16, 512, dtype=torch.bfloat16, device="cuda"))
+        lib.pa_latent_decode(outs[-1], None, *args, workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(*outs)
+    with pytest.raises(lib.PAError, match="WORKSPACE"):
+        lib.pa_latent_decode(outs[0], None, *args, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    q = _randn(g, 90, 2, 192).to(torch.bfloat16).cuda()
+    kv = _randn(g, 4000, 2, 256).to(torch.bfloat16).cuda()
+    kr = _randn(g, 4000, 64).to(torch.bfloat16).cuda()
+    t = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    need = lib.pa_latent_prefill_workspace_size(1, 90, 4000, 2, 128)
+    assert need > 0 and lib.pa_latent_prefill_workspace_size(8, 20000, 20000, 16, 128) == 0
+    outs = []
+    for fill in (0, 255):
+        outs.append(torch.empty(90, 2, 128, dtype=torch.bfloat16, device="cuda"))
+        lib.pa_latent_prefill(outs[-1], None, q, kv[..., :128], kr, kv[..., 128:], t(0, 90), t(0, 4000), 0.05, 90,
+                              workspace=torch.full((need,), fill, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(*outs)
+    with pytest.raises(lib.PAError, match="WORKSPACE"):
+        lib.pa_latent_prefill(outs[0], None, q, kv[..., :128], kr, kv[..., 128:], t(0, 90), t(0, 4000), 0.05, 90)
+    assert lib.pa_get_device_error() == 0
+
+
 def test_prefill_one_head_one_token(lib):
     _check_prefill(lib, [1], [1], 1, 128, "bf16")
     _check_prefill(lib, [1], [1], 1, 64, "f16", side_by_side=False)

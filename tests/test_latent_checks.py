@@ -107,7 +107,7 @@ def _decode(out=A, q=A + 16, s=1, tq=1, mq=1, h=16, r=512, d=64, bs=16, nb=4, sc
 
 def _prefill(out=A, q=A + 16, k=A, ks=256, kh=128, krs=64, s=1, tq=1, tk=1, mq=1, h=2, dn=128, dr=64, dv=128, scale=0.1, dt=2):
     return _lib.library().pa_latent_prefill(out, None, q, k, A, A, ks, kh, krs, 256, 128, A, A, s, tq, tk, mq, h, dn, dr, dv,
-                                            scale, 1, dt, None)
+                                            scale, 1, dt, None, 0, None)
 
 
 def test_library_refuses_write():
