@@ -225,6 +225,26 @@ def test_decode_more_rows_than_announced(lib):
     assert torch.all(out[:4] == 0) and torch.all(out[4:].abs().sum(-1) > 0)
 
 
+def test_a_cache_beyond_32_bit_offsets(lib):
+    """Rows written and read where the byte offset passes 2^32 (a pool of 5 GB)."""
+    from paged_kv_cache_388_b200.latent import PagedLatentCache
+    bs, nb, n = 64, 70000, 500
+    user = PagedLatentCache(nb, 512, 64, bs)
+    assert user.latent_cache.numel() * 2 > 5 * 10 ** 9
+    g = torch.Generator().manual_seed(1)
+    rows = _randn(g, n, 576).to(torch.bfloat16)
+    ids = torch.arange(nb - 8, nb, dtype=torch.int32).flip(0)  # the last blocks
+    pos = torch.arange(n)
+    slots = ids[pos // bs].long() * bs + pos % bs
+    user.write(rows[:, :512].cuda(), rows[:, 512:].cuda(), slots.cuda())
+    q = _randn(g, 1, 16, 576).to(torch.bfloat16)
+    out = user.attend(q.cuda(), ids[None].contiguous().cuda(), torch.tensor([n], dtype=torch.int32).cuda(), 0.05)
+    k = rows.double()
+    ref, lse, absolute, size = attend(q.double(), k[:, None], k[:, None, :512], torch.tensor([n]), 0.05)
+    assert torch.all((out.cpu().double() - ref).abs() <= bounds(ref, lse, absolute, size, n, 576, torch.bfloat16)[0])
+    assert lib.pa_get_device_error() == 0
+
+
 def test_decode_on_two_streams_and_captured(lib):
     """Two captured graphs and an eager call, replayed on different streams at once, each with its own result."""
     from paged_kv_cache_388_b200.latent import PagedLatentCache
@@ -311,6 +331,7 @@ def test_prefill_over_a_prefix(lib, dn):
 @pytest.mark.parametrize("dn", [128, 64])
 def test_prefill_rows_without_keys(lib, dn):
     # more rows than keys: the leading rows see nothing; and a sequence without any key
+    _check_prefill(lib, [300, 2], [0, 0], 2, dn, "f16")
     _check_prefill(lib, [200, 5, 3, 130], [150, 0, 1, 2], 2, dn, "bf16", pad_rows=4)
 
 
@@ -406,6 +427,34 @@ def test_prefill_infinities_behind_the_last_key(lib):
     kv[70:], kr[70:] = float("nan"), float("inf")
     got = latent_prefill(q, kv[..., :128], kr, kv[..., 128:], sl, sl, 0.07, **args)
     assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
+def test_prefill_on_two_streams_and_captured(lib):
+    """A split and a whole call captured, replayed on different streams at once."""
+    from paged_kv_cache_388_b200.latent import latent_prefill
+    g = torch.Generator().manual_seed(8)
+    graphs = []
+    for n, keys, heads in ((90, 6000, 2), (600, 600, 40)):
+        q = _randn(g, n, heads, 192).to(torch.bfloat16).cuda()
+        kv = _randn(g, keys, heads, 256).to(torch.bfloat16).cuda()
+        kr = _randn(g, keys, 64).to(torch.bfloat16).cuda()
+        qsl, ksl = (torch.tensor([0, x], dtype=torch.int32).cuda() for x in (n, keys))
+        args = (q, kv[..., :128], kr, kv[..., 128:], qsl, ksl, 0.05)
+        want = latent_prefill(*args, max_query_len=n)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = latent_prefill(*args, max_query_len=n)
+        graphs.append((gr, out, want, args))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for (gr, *_), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    for gr, out, want, _ in graphs:
+        assert torch.equal(out, want)
+    assert lib.pa_get_device_error() == 0
 
 
 def test_prefill_bad_offsets_are_reported(lib):
