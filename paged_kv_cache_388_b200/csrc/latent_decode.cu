@@ -9,18 +9,18 @@
 // memory and used by two products.
 //
 // A CTA holds NR query rows (16, 32 or 64) in shared memory and streams tiles
-// of 64 keys.  What shapes the products is tensor memory: 128 rows of R = 512
-// fp32 sums would fill all of its 512 columns and leave none for S, so the
-// second product is turned round:
-//     S   [rows x keys] = Q C^T           M 64, N 64, K R+64
-//     O^T [values x rows] += C^T P^T      M 128 (R/128 times), N NR, K 64
+// of KT keys (32 for R = 512, 64 for 256).  What shapes the products is tensor
+// memory: 128 rows of R = 512 fp32 sums would fill all of its 512 columns and
+// leave none for S, so the second product is turned round:
+//     S   [rows x keys] = Q C^T           M 64, N KT, K R+64
+//     O^T [values x rows] += C^T P^T      M 128 (R/128 times), N NR, K KT
 // O^T takes NR columns per 128 values (256 columns at NR 64, R 512) beside two
-// 64-column buffers of S.  A row of S lies in one thread (lanes 0-15 of each
-// warp's quarter hold 16 rows), so the softmax needs no exchange; P goes to
-// shared memory in the K-major layout that the B operand wants.  C is read
-// from shared memory as it lies: K-major for S, values-contiguous as the A
-// operand of O^T.  S(j+1) is issued before the product of P(j), so the
-// softmax runs under it.
+// buffers of S.  A row of S lies in four threads of a warp (its quarter holds 16
+// rows, read as 16 lanes x KT columns so that all 32 threads have work), so the
+// softmax needs two shuffles and, for the rare rescaling of O^T, whose rows lie
+// across all threads, one vote.  P goes to shared memory in the K-major layout
+// that the B operand wants.  C is read from shared memory as it lies: K-major
+// for S, values-contiguous as the A operand of O^T.
 //
 // Keys arrive by TMA through the block table, one box a block: a 4-D view of
 // the cache splits rows into groups of 8 and each row into 64-value pieces, so
@@ -28,13 +28,16 @@
 // between groups across the blocks of a tile.
 //
 // Work split: the tiles of all sequences form one line that is cut into equal
-// ranges, one per worker (ceil(rows / NR) CTAs, one per row tile, read the same
-// keys at the same time).  A sequence that lies in one range is written at
-// once; a cut one leaves a record (sums, maximum, total) per range, and the
-// merge kernel joins them in the order of the ranges.
+// ranges (see Line).  A sequence that lies in one range is written at once; a
+// cut one leaves a record (sums, maximum, total) per range, and the merge kernel
+// joins them in the order of the ranges.
 //
-// Bound: memory (each row of the cache once) up to about 64 rows a sequence,
-// beyond that the tensor cores.
+// Bound: memory (each row of the cache once) up to about 32 rows a sequence: 256
+// ragged sequences of 16 heads and 512 values, 320 MB, take 70 us (4.6 TB/s with
+// the merge, tiles arriving at 7 TB/s in between); beyond that the issue of S (36
+// products a tile, 28 cycles each): 64 sequences of 2048 to 8192 keys and 128
+// heads take 146 us (655 TFLOP/s).  With 256 values a tile's softmax is the
+// longest step (1800 cycles for 64 rows x 64 keys).
 #include <limits.h>
 
 #include "latent.h"
@@ -50,6 +53,7 @@ constexpr int kThreads = 224;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kBadSlots = 16;  // more than the items the producer can be ahead by
 constexpr int kMaxStages = 6;
+
 // KT keys a tile
 template <int R, int NR, int KT>
 struct Shape {
@@ -111,8 +115,8 @@ struct Seq {
 
 // How the work is laid out in a line of units: an item (a sequence's tiles for
 // one row tile) has one unit a tile and `extra` for what it costs beside them.
-// Lockstep: a sequence is one item and each worker is `lanes` CTAs, one per row tile,
-// that read the same keys at the same time (one of them from memory).  Flat
+// Lockstep: a sequence is one item and each worker is `lanes` CTAs, one per row
+// tile, that read the same keys at the same time (one of them from memory).  Flat
 // (lanes 1): a sequence is an item per row tile it really has, and a worker is
 // one CTA; for batches whose sequences differ in rows.
 struct Line {
