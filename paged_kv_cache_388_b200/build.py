@@ -35,11 +35,12 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-# The test build of the decode kernel: a 50 ms wait limit and one ring use of
-# CTA 0 announced but never copied, so that a test can watch a wait expire and
-# the kernel unwind with PA_DEVERR_TIMEOUT (tests/test_wait_timeout.py).
+# The test build of the kernels that wait for copies: a 50 ms wait limit and one
+# ring use of CTA 0 announced but never copied, so that a test can watch a wait
+# expire and the kernel unwind with PA_DEVERR_TIMEOUT (tests/test_wait_timeout.py,
+# tests/test_latent_wait_timeout.py).
 WAITTEST_LIB = os.path.join(PKG, "libpa_waittest.so")
-WAITTEST_SRC = "decode_mma.cu"
+WAITTEST_SRCS = ("decode_mma.cu", "latent_decode.cu", "latent_prefill.cu")
 WAITTEST_DEFINES = ["-DPA_WAIT_LIMIT_NS=50000000ull", "-DPA_TEST_LOST_COPY=3"]
 
 
@@ -64,13 +65,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
-    wt_src = os.path.join(CSRC, WAITTEST_SRC)
-    jobs = [(s, (), "") for s in srcs] + [(wt_src, WAITTEST_DEFINES, ".waittest")]
+    wt = [(os.path.join(CSRC, s), WAITTEST_DEFINES, ".waittest") for s in WAITTEST_SRCS]
+    jobs = [(s, (), "") for s in srcs] + wt
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         built = list(ex.map(lambda j: _compile(j[0], verbose, j[1], j[2]), jobs))
-    objs, wt_obj = built[:-1], built[-1]
+    objs, wt_objs = built[:-len(wt)], built[-len(wt):]
     _link(LIB, objs)
-    _link(WAITTEST_LIB, [o for o in objs if os.path.basename(o) != WAITTEST_SRC + ".o"] + [wt_obj])
+    _link(WAITTEST_LIB, [o for o in objs if os.path.basename(o)[:-2] not in WAITTEST_SRCS] + wt_objs)
     return LIB
 
 

@@ -364,6 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) mbar_arrive_expect_tx(&bars[kFull + st], nb * kBox * SH::kD * 2);
         __syncwarp();
+#ifdef PA_TEST_LOST_COPY
+        // test build only: tile PA_TEST_LOST_COPY of CTA 0 is announced on its
+        // barrier but never copied, so that the waits for it expire
+        if (blockIdx.x == 0 && g == (uint32_t)PA_TEST_LOST_COPY) continue;
+#endif
         if (lane < nb)  // a bad id is replaced by a valid block
           tma_load_4d(sbase + SH::kOffStage + st * SH::kStage + lane * (kBox / 8) * SH::kGroup, &tmc, 0, 0, 0,
                       (wrong ? 0 : id) * (BS / 8) + (key % BS) / 8, &bars[kFull + st]);
@@ -373,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every copy has landed before the CTA can exit
     if (lane == 0) {
-      bool landed = drain_ring(&bars[kFull], SH::kStages, g) && drain_ring(&bars[kQFull], SH::kQBufs, item);
-      if (!landed) fail();
+      const bool keys = drain_ring(&bars[kFull], SH::kStages, g), queries = drain_ring(&bars[kQFull], SH::kQBufs, item);
+      if (!keys || !queries) fail();
     }
   } else if (warp == kSWarp) {
     // ======================= S = Q C^T ======================================
@@ -460,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pr = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
     const uint32_t prow = (pr >> 3) * 1024 + (pr & 7) * 128;
     uint32_t g = 0, item = 0;
+    bool ok = true;
     while (walk.next()) {
       const Seq x = walk.x;
       const int first_row = walk.first_row;
@@ -473,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         limit[i] = valid[i] ? min(x.L - x.Q + (first_row + r0 + 8 * i) / H, x.L - 1) : -1;
       }
       const int limit_lo = min(x.L - x.Q + first_row / H, x.L - 1);  // the tile's least
-      bool ok = true;
       for (int j = walk.t0; j < walk.t1; ++j, ++g) {
         // after a failed wait the loop runs on without waiting, so that the
         // four warps keep meeting at their barrier

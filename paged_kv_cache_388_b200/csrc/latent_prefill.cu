@@ -381,6 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t *bar = &bars[(c < SH::kKC ? kKFull : kVFull) + p];
             if (c == 0) mbar_arrive_expect_tx(bar, SH::kKC * kChunk);
             if (c == SH::kKC) mbar_arrive_expect_tx(bar, SH::kVC * kChunk);
+#ifdef PA_TEST_LOST_COPY
+            // test build only: the first chunk of tile PA_TEST_LOST_COPY of CTA 0
+            // is announced but never copied, so that the waits for it expire
+            if (worker == 0 && x == (uint32_t)(PA_TEST_LOST_COPY * SH::kTC)) {
+            } else
+#endif
             if (c < SH::kKC - 1) tma_load_3d(dst, &tmk, c * 64, it.head, row, bar);
             else if (c == SH::kKC - 1) tma_load_2d(dst, &tmr, 0, row, bar);
             else tma_load_3d(dst, &tmv, (c - SH::kKC) * 64, it.head, row, bar);

@@ -141,14 +141,14 @@ __device__ __forceinline__ void umma_ts_lo(uint32_t tmem_d, uint32_t tmem_a, uin
       : "memory");
 }
 
-// Poll a barrier up to 4096 times in a loop of three instructions.  The wait
+// Poll a barrier up to 256 times in a loop of three instructions.  The wait
 // stands in many places of a kernel whose roles share the instruction cache:
 // inlined with its clock and its failure path it took 330 cycles on a barrier
 // that had long completed, this loop 40.
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 4096;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 256;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra.uni DONE_%=;\n\t"
       "POLL_%=:\n\t"
