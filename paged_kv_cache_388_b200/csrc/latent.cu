@@ -186,6 +186,8 @@ int pa_latent_prefill(void *out, float *lse, const void *q, const void *k, const
   for (int i = 0; i < 5; ++i)
     if (strides[i] <= 0 || strides[i] % 8 || strides[i] >= (int64_t)1 << 38) return PA_ERR_INVALID_ARG;
   if (out == q) return PA_ERR_INVALID_ARG;
+  if ((int64_t)num_q_tokens * num_heads > (int64_t)1 << 30 || (int64_t)num_seqs * num_heads > (int64_t)1 << 30)
+    return PA_ERR_UNSUPPORTED;
   if (max_query_len > num_q_tokens) max_query_len = num_q_tokens;
   DevInfo dev;
   if (device_info(&dev) != cudaSuccess) return PA_ERR_CUDA;

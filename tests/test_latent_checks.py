@@ -132,7 +132,7 @@ def test_library_refuses_prefill():
     for bad in (dict(scale=float("nan")), dict(scale=-1.0), dict(h=0), dict(mq=0), dict(out=None), dict(q=A), dict(k=A + 2),
                 dict(ks=100), dict(kh=0), dict(krs=-64), dict(k=None)):
         assert _prefill(**bad) == INVALID, bad
-    for bad in (dict(dn=96, dv=96), dict(dv=64), dict(dr=32), dict(dt=0)):
+    for bad in (dict(dn=96, dv=96), dict(dv=64), dict(dr=32), dict(dt=0), dict(tq=1 << 20, h=1 << 11)):
         assert _prefill(**bad) == UNSUPPORTED, bad
 
 
