@@ -202,6 +202,61 @@ def test_a_captured_step_runs_on_by_itself():
 
 
 @gpu
+def test_seventy_pools_follow():
+    """More pools than a launch takes: K and V of 35 layers."""
+    from paged_kv_cache_388_b200 import _lib
+    tables, lens, refs = [[5, 0], [5, 0], [9, 8]], [10, 10, 20], [0] * 40
+    for b, c in ((5, 2), (9, 1), (8, 1)):
+        refs[b] = c
+    dev = _device(tables, lens, refs, 16)
+    pools = [torch.randint(0, 255, (40, 16 + 16 * (i % 5)), dtype=torch.uint8) for i in range(70)]
+    dpools = [p.cuda() for p in pools]
+    _, _, pairs = dev.step(_i32([1, 1, 0]), 2, pools=dpools)
+    want = model.step(tables, lens, refs, [1, 1, 0], 16, 2)[2]
+    assert [tuple(p) for p in pairs.tolist()] == want and want[0] == (5, 0)
+    _, moves = dev.compact(pools=dpools)
+    for s, t in want + model.compact(tables, lens, refs, 16)[1]:
+        if s >= 0:
+            for p in pools:
+                p[t] = p[s]
+    assert dev.block_tables.tolist() == tables and dev.ref_counts.tolist() == refs
+    for p, d in zip(pools, dpools):
+        assert torch.equal(d.cpu(), p)
+    assert _lib.pa_get_device_error() == 0
+
+
+@gpu
+def test_two_tables_at_once():
+    """Steps and compactions of two tables on two streams, each against its own model."""
+    from paged_kv_cache_388_b200 import _lib
+    r = random.Random(3)
+    both = []
+    for rows, width, nb in ((300, 20, 9000), (40, 30, 70000)):
+        tables, lens, refs = _state(r, rows, width, nb, 16, 60)
+        both.append([tables, lens, refs, _device(tables, lens, refs, 16), torch.cuda.Stream(),
+                     torch.zeros(nb, 1024, dtype=torch.uint8, device="cuda")])
+    torch.cuda.synchronize()
+    for _ in range(4):
+        todo = []
+        for t in both:
+            append = [r.randint(0, 20) for _ in t[1]]
+            release = [int(r.random() < 0.2) for _ in t[1]]
+            todo.append((append, release, _i32(append), _i32(release)))
+        torch.cuda.synchronize()
+        for (append, release, da, dr), (_, _, _, dev, st, pool) in zip(todo, both):
+            with torch.cuda.stream(st):
+                dev.step(da, sum(append), release=dr, pools=[pool])
+                dev.compact(pools=[pool])
+        torch.cuda.synchronize()
+        for (append, release, _, _), (tables, lens, refs, dev, _, _) in zip(todo, both):
+            model.step(tables, lens, refs, append, 16, 0, release)
+            model.compact(tables, lens, refs, 16)
+            assert dev.block_tables.tolist() == tables and dev.ref_counts.tolist() == refs
+            assert dev.context_lens.tolist() == lens
+    _lib.pa_get_device_error()
+
+
+@gpu
 def test_from_the_host_allocator():
     from paged_kv_cache_388_b200.tables import DeviceBlockTables
     al = BlockAllocator(50, 16, free_order=reversed(range(50)))
