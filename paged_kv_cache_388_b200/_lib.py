@@ -632,7 +632,7 @@ def pa_latent_prefill(out, lse, q, k, k_rope, v, query_start_loc, context_start_
 def _table_shapes(block_tables, context_lens, ref_counts):
     if not (block_tables.dim() == 2):
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    if not (tuple(context_lens.shape) == (block_tables.shape[0],)):
+    if context_lens.dim() != 1 or context_lens.shape[0] != block_tables.shape[0]:
         raise ValueError("block_tables and context_lens disagree on the number of sequences")
     if not (ref_counts.dim() == 1):
         raise ValueError("ref_counts must be [num_blocks]")
@@ -654,7 +654,7 @@ def _pool_args(pools, num_blocks, cur):
         if not (t.dim() >= 1 and t.shape[0] == num_blocks):
             raise ValueError(f"a pool must hold {num_blocks} blocks, got {tuple(t.shape)}")
         ptrs[i] = t.data_ptr()
-        sizes[i] = t.stride(0) * t.element_size() if num_blocks > 1 else t.numel() * t.element_size()
+        sizes[i] = t.nbytes // num_blocks
     return ptrs, sizes, n
 
 
@@ -670,11 +670,6 @@ def pa_table_step(block_tables, context_lens, ref_counts, append, block_size, sl
     int64 [max_new_tokens], query_start_loc int32 [S + 1] and copy_pairs int64
     [S, 2] are written; pools: CUDA tensors [NB, ...] whose blocks follow."""
     s, w, nb, cur = _table_shapes(block_tables, context_lens, ref_counts)
-    for name, t in (("append", append), ("release", release), ("fork_src", fork_src)):
-        if t is not None:
-            if not (tuple(t.shape) == (s,)):
-                raise ValueError(f"{name} must hold one entry per sequence")
-            _dev(t, name, torch.int32, cur)
     if not (slot_mapping.dim() == 1):
         raise ValueError("slot_mapping must be [max_new_tokens]")
     if not (tuple(query_start_loc.shape) == (s + 1,)):
@@ -684,14 +679,29 @@ def pa_table_step(block_tables, context_lens, ref_counts, append, block_size, sl
     _dev(slot_mapping, "slot_mapping", torch.int64, cur)
     _dev(query_start_loc, "query_start_loc", torch.int32, cur)
     _dev(copy_pairs, "copy_pairs", torch.int64, cur)
-    ptrs, sizes, n = _pool_args(pools, nb, cur)
     if workspace is not None:
         _dev(workspace, "workspace", None, cur)
+    _table_step((s, w, nb, cur), block_tables, context_lens, ref_counts, append, block_size,
+                slot_mapping, query_start_loc, copy_pairs, release, fork_src, pools, workspace,
+                stream)
+
+
+def _table_step(sizes, block_tables, context_lens, ref_counts, append, block_size, slot_mapping,
+                query_start_loc, copy_pairs, release, fork_src, pools, workspace, stream):
+    """pa_table_step with tables checked (sizes: _table_shapes') and outputs and
+    workspace that are the caller's own."""
+    s, w, nb, cur = sizes
+    for name, t in (("append", append), ("release", release), ("fork_src", fork_src)):
+        if t is not None:
+            if t.dim() != 1 or t.shape[0] != s:
+                raise ValueError(f"{name} must hold one entry per sequence")
+            _dev(t, name, torch.int32, cur)
+    ptrs, block_bytes, n = _pool_args(pools, nb, cur)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = _lib.pa_table_step(_ptr(block_tables), w, _ptr(context_lens), _ptr(ref_counts),
                             _ptr(release), _ptr(fork_src), _ptr(append), s, nb, int(block_size),
                             _ptr(slot_mapping), slot_mapping.shape[0], _ptr(query_start_loc),
-                            _ptr(copy_pairs), ptrs, sizes, n, _ptr(workspace), ws_bytes,
+                            _ptr(copy_pairs), ptrs, block_bytes, n, _ptr(workspace), ws_bytes,
                             _stream(stream))
     _check(rc, "pa_table_step")
 
@@ -708,13 +718,21 @@ def pa_table_compact(block_tables, context_lens, ref_counts, block_size, num_liv
         raise ValueError("block_moves must be [max(1, num_blocks // 2), 2]")
     _dev(num_live, "num_live", torch.int32, cur)
     _dev(block_moves, "block_moves", torch.int64, cur)
-    ptrs, sizes, n = _pool_args(pools, nb, cur)
     if workspace is not None:
         _dev(workspace, "workspace", None, cur)
+    _table_compact((s, w, nb, cur), block_tables, context_lens, ref_counts, block_size, num_live,
+                   block_moves, pools, workspace, stream)
+
+
+def _table_compact(sizes, block_tables, context_lens, ref_counts, block_size, num_live, block_moves,
+                   pools, workspace, stream):
+    """pa_table_compact, as _table_step."""
+    s, w, nb, cur = sizes
+    ptrs, block_bytes, n = _pool_args(pools, nb, cur)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = _lib.pa_table_compact(_ptr(block_tables), w, _ptr(context_lens), _ptr(ref_counts), s, nb,
-                               int(block_size), _ptr(num_live), _ptr(block_moves), ptrs, sizes, n,
-                               _ptr(workspace), ws_bytes, _stream(stream))
+                               int(block_size), _ptr(num_live), _ptr(block_moves), ptrs, block_bytes,
+                               n, _ptr(workspace), ws_bytes, _stream(stream))
     _check(rc, "pa_table_compact")
 
 

@@ -62,22 +62,24 @@ class DeviceBlockTables:
         int64 [num_seqs, 2]; the copies are done in all ``pools`` ([num_blocks,
         ...] tensors).  When the pool runs out the row and all later growing
         ones stay as they are (PA_DEVERR_POOL in the device error word)."""
-        n, t = self.num_seqs, self.block_tables
+        t = self.block_tables
+        sizes = _lib._table_shapes(t, self.context_lens, self.ref_counts)
+        n = sizes[0]
         slots = t.new_empty(max_new_tokens, dtype=torch.int64)
         qsl = t.new_empty(n + 1)
         pairs = t.new_empty((n, 2), dtype=torch.int64)
-        _lib.pa_table_step(self.block_tables, self.context_lens, self.ref_counts, append,
-                           self.block_size, slots, qsl, pairs, release=release, fork_src=fork_src,
-                           pools=pools, workspace=self._ws)
+        _lib._table_step(sizes, t, self.context_lens, self.ref_counts, append, self.block_size,
+                         slots, qsl, pairs, release, fork_src, pools, self._ws, None)
         return slots, qsl, pairs
 
     def compact(self, pools=()):
         """Move the used blocks to ids [0, live) in the tables and in all
         ``pools``.  Returns live (int32 [1]) and the moves (src, dst), int64
         [max(1, num_blocks // 2), 2] filled up with (-1, -1)."""
-        live = self.block_tables.new_empty(1)
-        moves = self.block_tables.new_empty((max(1, self.num_blocks // 2), 2), dtype=torch.int64)
-        _lib.pa_table_compact(self.block_tables, self.context_lens, self.ref_counts,
-                              self.block_size, live, moves, pools=pools,
-                              workspace=self._ws)
+        t = self.block_tables
+        sizes = _lib._table_shapes(t, self.context_lens, self.ref_counts)
+        live = t.new_empty(1)
+        moves = t.new_empty((max(1, sizes[2] // 2), 2), dtype=torch.int64)
+        _lib._table_compact(sizes, t, self.context_lens, self.ref_counts, self.block_size, live,
+                            moves, pools, self._ws, None)
         return live, moves
