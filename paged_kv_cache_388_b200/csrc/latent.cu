@@ -11,20 +11,21 @@ namespace {
 
 // One thread per 16-byte vector of a token's row: the first `lv` vectors come
 // from the latent part, the rest from the rope part.  Reads and writes are
-// coalesced within a row of 576 or 1152 bytes.  Bound: memory traffic and, for
-// a decode step's few tokens, the latency of one dependent load (the slot).
+// coalesced within a row of 640 or 1152 bytes.  I: the type that counts vectors
+// (64-bit divisions make 16411 rows of 1152 bytes 8.4 us instead of 6.6).  Bound: memory traffic
+// and, for a decode step's few tokens, the latency of one dependent load (the
+// slot).
+template <typename I>
 __global__ void __launch_bounds__(256) latent_write_kernel(
     const uint4 *__restrict__ latent, const uint4 *__restrict__ rope, uint4 *__restrict__ cache,
     const int64_t *__restrict__ slots, int num_tokens, int64_t latent_stride, int64_t rope_stride,
     int lv, int rv, int64_t num_slots, unsigned int *err) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int row = lv + rv;
-  const int64_t total = (int64_t)num_tokens * row;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
+  const I row = (I)(lv + rv), total = (I)num_tokens * row;
+  for (I i = (I)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (I)gridDim.x * blockDim.x) {
     const int64_t t = i / row;
-    const int v = (int)(i - t * row);
+    const int v = (int)(i - (I)t * row);
     const uint4 x = __ldcs(v < lv ? latent + t * latent_stride + v : rope + t * rope_stride + (v - lv));
     const int64_t slot = slots[t];
     if (slot < 0) continue;  // padding token
@@ -32,7 +33,7 @@ __global__ void __launch_bounds__(256) latent_write_kernel(
       if (v == 0) raise_error(err, PA_DEVERR_SLOT);
       continue;
     }
-    cache[slot * row + v] = x;
+    cache[slot * (lv + rv) + v] = x;
   }
 }
 
@@ -85,8 +86,11 @@ int pa_latent_write(const void *latent, const void *rope, void *latent_cache,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // below 2^31 vectors the loop's last step stays below 2^32 too
+  const bool narrow = (int64_t)num_tokens * (lv + rv) < (int64_t)1 << 31;
   const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, latent_write_kernel, static_cast<const uint4 *>(latent), static_cast<const uint4 *>(rope),
+      &cfg, narrow ? latent_write_kernel<uint32_t> : latent_write_kernel<uint64_t>,
+      static_cast<const uint4 *>(latent), static_cast<const uint4 *>(rope),
       static_cast<uint4 *>(latent_cache), slot_mapping, num_tokens, latent_stride / 8, rope_stride / 8,
       lv, rv, (int64_t)num_blocks * block_size, dev.err);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

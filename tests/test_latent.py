@@ -245,6 +245,24 @@ def test_a_cache_beyond_32_bit_offsets(lib):
     assert lib.pa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("latent_dim, tokens", [(512, 29826200), (256, 53687200)])
+def test_write_of_more_vectors_than_31_bits(lib, latent_dim, tokens):
+    """More than 2^31 16-byte vectors in one call: one row for all tokens, nearly all of them padding."""
+    from paged_kv_cache_388_b200.latent import PagedLatentCache
+    row = latent_dim + 64
+    assert tokens * (row // 8) > 2 ** 31
+    user = PagedLatentCache(4, latent_dim, 64, 16)
+    user.latent_cache.fill_(-1.0)
+    one = _randn(torch.Generator().manual_seed(4), 1, row).to(torch.bfloat16).cuda()
+    slots = torch.full((tokens,), -1, dtype=torch.int64, device="cuda")
+    slots[0], slots[tokens // 2 + 1], slots[tokens - 1] = 3, 17, 63
+    user.write(one[:, :latent_dim].expand(tokens, -1), one[:, latent_dim:].expand(tokens, -1), slots)
+    want = torch.full((64, row), -1.0, dtype=torch.bfloat16, device="cuda")
+    want[[3, 17, 63]] = one
+    assert torch.equal(user.latent_cache.view(64, row), want)
+    assert lib.pa_get_device_error() == 0
+
+
 def test_decode_on_two_streams_and_captured(lib):
     """Two captured graphs and an eager call, replayed on different streams at once, each with its own result."""
     from paged_kv_cache_388_b200.latent import PagedLatentCache
