@@ -47,7 +47,7 @@
 namespace pa {
 namespace {
 
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8 between rescales
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^(8 + headroom) between rescales
 constexpr int kProducerWarp = 4, kSWarp = 5, kPvWarp = 6;
 constexpr int kThreads = 224;
 constexpr int kMaxSmem = 227 * 1024;
@@ -517,9 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 sl2x2 = make_float2(sl2, sl2);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            // lazy rescale: the reference moves when the tile's maximum exceeds
-            // it by more than 2^8 (first tile with a visible key: always)
-            const float top = mx[i] * sl2;
+            // lazy rescale: the reference moves when the tile's maximum, kHeadroom
+            // below it, exceeds it by more than 2^8 (first tile with a visible
+            // key: always)
+            const float top = mx[i] * sl2 - TT::kHeadroom;
             const bool up = valid[i] && top > m[i] + kRescaleThreshold;
             need = need || up;
             alpha[i] = up ? (m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - top)) : 1.f;
@@ -528,8 +529,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             negx2[i] = make_float2(-ref, -ref);
             psum[i] = make_float2(0.f, 0.f);
           }
-          // the sum takes the unrounded weights, the product P rounded to 16
-          // bits: half a step a weight, of the size of the result's own rounding
+          // The sum takes the unrounded weights, the product P rounded to 16
+          // bits: half a step a weight, of the size of the result's own rounding.
+          // f16 weights that fall below its normal range lose at most 2^-25 each,
+          // 2^-32 of the largest with the headroom (a million keys: 2^-12).
 #pragma unroll
           for (int k = 0; k < kG; ++k)
 #pragma unroll
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 e = __ffma2_rn(v, sl2x2, negx2[i]);
               const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
               psum[i] = __fadd2_rn(psum[i], p);
-              w[2 * k + i] = TT::pack(p.x, p.y);
+              w[2 * k + i] = TT::weights(p.x, p.y);
             }
 #pragma unroll
           for (int i = 0; i < 2; ++i) l[i] = l[i] * alpha[i] + (psum[i].x + psum[i].y);

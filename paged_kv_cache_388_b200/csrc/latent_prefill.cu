@@ -4,7 +4,8 @@
 // Head h of a token has a key [k_nope (DN) | k_rope (64, shared by the heads)]
 // and a value of DN; row t of a sequence with Q rows and L keys sees the keys
 // j <= L-Q+t (causal) or all of them.  With S = scale * Q K^T (base 2 below),
-// a running maximum m and sum l per row, O = sum_j 2^(s_j - m) v_j:
+// a running reference m (the maximum, less a headroom) and sum l per row, O =
+// sum_j 2^(s_j - m) v_j:
 //     out = O / l,  lse = (m + log2 l) ln 2.
 //
 // An item is (sequence, head, 256 query rows held as two Q tiles of 128).  Per
@@ -45,7 +46,7 @@ constexpr int kRows = 128;  // rows per Q tile (MMA M)
 constexpr int kKeys = 128;  // keys per tile
 constexpr int kQTiles = 2;
 constexpr int kChunk = 128 * 64 * 2;       // bytes of 128 rows x 64 columns
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8 between rescales
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^(8 + headroom) between rescales
 constexpr int kSoftmaxWarps = 4 * kQTiles;
 constexpr int kProducerWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kQTiles);
@@ -594,10 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; i += 2)
 #pragma unroll
           for (int c = 0; c < 2; ++c) m2[c] = fmax3(m2[c], __uint_as_float(s0[c][i]), __uint_as_float(s0[c][i + 1]));
-        const float mx = fmaxf(m2[0], m2[1]) * sl2;
-        // lazy rescale: move the reference only when the tile's maximum exceeds
-        // it by more than 2^8 (first tile with a visible key: always).  O_t is
-        // at rest here: S_t(j) was issued after P V of tile j-1 completed.
+        const float mx = fmaxf(m2[0], m2[1]) * sl2 - TT::kHeadroom;
+        // lazy rescale: move the reference only when the tile's maximum, kHeadroom
+        // below it, exceeds it by more than 2^8 (first tile with a visible key:
+        // always).  O_t is at rest here: S_t(j) was issued after P V of tile j-1
+        // completed.
         const bool need = mx > m + kRescaleThreshold;
         float alpha = 1.f;
         if (need) {
@@ -630,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P = 2^(s * scale * log2 e - m), key pairs in packed arithmetic; the sum
         // takes the unrounded weights (lse keeps fp32 accuracy), the product P
         // rounded to 16 bits: an error of half a step a weight, of the size of
-        // the result's own rounding
+        // the result's own rounding.  f16 weights that fall below its normal range
+        // lose at most 2^-25 each, 2^-32 of the largest with the headroom.
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 sl2x2 = make_float2(sl2, sl2), negx2 = make_float2(-ref, -ref);
         float2 psum = make_float2(0.f, 0.f);
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 e = __ffma2_rn(x, sl2x2, negx2);
             const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
             psum = __fadd2_rn(psum, p);
-            w[i >> 4][i & 15] = TT::pack(p.x, p.y);
+            w[i >> 4][i & 15] = TT::weights(p.x, p.y);
           }
           // over columns already read: keys 64 hf .. go to columns 32 hf ..
           tmem_st16(ts + 32 * hf, w[0]);

@@ -19,6 +19,11 @@ struct TcType<__nv_bfloat16> {
   static constexpr uint32_t kFmt = 1;  // instruction-descriptor a/b format: BF16
   static constexpr bool kSplitP = true;
   static constexpr CUtensorMapDataType kTma = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  // How far, in powers of two, the reference of the latent kernels' softmax lies
+  // below a tile's maximum: bf16 weights have fp32's range and need none.
+  static constexpr float kHeadroom = 0.f;
+  // Two softmax weights as operand of the second product.
+  __device__ __forceinline__ static uint32_t weights(float a, float b) { return pack(a, b); }
   __device__ __forceinline__ static uint32_t pack(float a, float b) {
     __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -35,6 +40,18 @@ template <>
 struct TcType<__half> {
   static constexpr uint32_t kFmt = 0;  // F16
   static constexpr bool kSplitP = false;
+  // f16 weights of a maximum of 1 would be subnormal below 2^-14 and 0 below
+  // 2^-25, so that many keys 17 or more below one strong one vanished from the
+  // product while the sum counted them.  With the maximum at 2^7, and 2^8 more
+  // until a rescale, the largest weight is 2^15, below the largest f16 (2^16).
+  static constexpr float kHeadroom = 7.f;
+  // (saturating: beyond logits of 2^22 the reference's own rounding may lift a
+  // weight past the largest f16)
+  __device__ __forceinline__ static uint32_t weights(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+  }
   static constexpr CUtensorMapDataType kTma = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   __device__ __forceinline__ static uint32_t pack(float a, float b) {
     __half2 v = __floats2half2_rn(a, b);
