@@ -588,7 +588,8 @@ size_t pa_latent_decode_workspace_size(int num_seqs, int max_query_len,
  * v_dim in {64, 128}, rope_dim 64, PA_F16 and PA_BF16, scale finite and >= 0.
  * Device checks: offsets out of range or more than max_query_len rows set
  * PA_DEVERR_QUERY_LEN (a sequence with more rows: zeros; offsets out of range:
- * skipped).  Keys and values of tokens that only some rows of a sequence see
+ * skipped; where query_start_loc goes back, sequences beside that place may be
+ * skipped too).  Keys and values of tokens that only some rows of a sequence see
  * must be finite.  Rows past the last sequence are left as they are.
  */
 int pa_latent_prefill(void *out, float *lse, const void *q, const void *k,

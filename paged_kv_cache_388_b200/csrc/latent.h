@@ -5,6 +5,31 @@
 
 namespace pa {
 
+// Ragged batches laid out in places: sequence s, whose rows begin at `start[s]`
+// (times `mul`), has the places first_place(s) and following, one for every
+// per = 2^shift of its rows.  n rows need ceil(n / per) places, and
+// ceil(n / per) <= (begin + n) / per - begin / per + 1, so sequences never share
+// one, all places lie below rows / per + num_seqs, and whose a place is follows
+// from the offsets alone, without a sum over the sequences.
+__device__ __forceinline__ int64_t first_place(const int32_t *start, int s, int mul, int shift) {
+  return ((int64_t)start[s] * mul >> shift) + s;
+}
+// The last sequence whose places begin at or before `place`; a whole warp asks,
+// 32 sequences at a time.  (Offsets that go back give some sequence: callers
+// compare the place with the sequence's own.)
+__device__ __forceinline__ int seq_of_place(const int32_t *start, int num_seqs, int mul, int shift, int64_t place) {
+  int lo = 0, n = num_seqs;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = (int)(threadIdx.x & 31) * step;
+    const bool at = i < n && first_place(start, lo + i, mul, shift) <= place;
+    const int before = __popc(__ballot_sync(0xffffffffu, at));
+    const int skip = before > 0 ? (before - 1) * step : 0;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
+  }
+  return lo;
+}
+
 // Absorbed form over the paged latent cache (latent_decode.cu).
 struct LatentArgs {
   void *out;    // [Tq][H][latent_dim]

@@ -17,7 +17,7 @@
 // one lies under the products of the other.
 //
 // Work split.  Where there are items enough to fill the machine a CTA takes one
-// item, those with the most keys first.  Few rows over a long prefix would keep
+// item, those with the most keys first (see kMostEmpty).  Few rows over a long prefix would keep
 // a few SMs busy: there the key tiles of all items form one line (with one unit
 // more an item, for its queries and its epilogue) that is cut into equal ranges,
 // one a CTA; an item that lies in one range is written at once, a cut one leaves
@@ -84,7 +84,17 @@ __device__ __forceinline__ void mask_keys(uint32_t (&s)[2][32], int last) {
 
 constexpr int kExtra = 1;       // units an item has beside its tiles
 constexpr int kMinUnits = 3;    // units a worker is worth
-constexpr int kPairRows = kQTiles * kRows;
+constexpr int kPairRows = kQTiles * kRows, kPairShift = 8;
+static_assert(kPairRows == 1 << kPairShift, "rows of an item");
+// CTAs of the grid of pairs for each of the grid of places, at most.  A CTA
+// without an item holds an SM's shared memory for a microsecond, and there is one
+// for every pair that the longest sequence has and another has not: a prompt of
+// 8192 rows among 255 single rows, 128 heads, took 10.9 ms by pairs and takes 4.1
+// by places, nine prompts of 1000 rows announced as 9000 133 and 108 us.  Where few
+// are empty pairs are as fast or faster, the longest items of all sequences being
+// first (64 prompts of 128 rows 79 against 82 us, nine of 1000 104 against 109; 32
+// of 1 to 2048, nearly half of the CTAs empty, 414 against 398).
+constexpr int kMostEmpty = 2;
 constexpr int kSplitTokens = 1024;  // keys of all sequences below which no item is cut
 
 // A cut item's piece, as its worker leaves it for the joining kernel.
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap tmq,
                           const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmr,
                           const __grid_constant__ CUtensorMap tmv, float *rec, float2 *rec_ml, Piece *pieces,
-                          int pairs /* not SPLIT: items of a sequence and head, at most */) {
+                          int pairs /* not SPLIT: items of a sequence and head, at most; 0: CTAs by places */) {
   using TT = TcType<T>;
   using SH = Shape<DN>;
   extern __shared__ unsigned char smem_raw[];
@@ -263,16 +273,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t lo = 0, hi = 0;
   Item it;  // the CTA's one item, or the item that a role's walk has come to
   if constexpr (!SPLIT) {
-    // ---- the CTA's item; those with the most keys come first ----------------
-    const int per_pair = a.num_seqs * H, pair = pairs - 1 - worker / per_pair;
-    const Seq x = seq_of(a, worker % per_pair / H, tid == 0 ? a.err : nullptr);
-    if (pair >= x.pairs) return;  // CTA-uniform, before tensor memory is taken
+    // ---- the CTA's item; those with the most keys come first (by places: first
+    // within their sequence) ---------------------------------------------------
+    int seq, pair, step;
+    if (pairs) {
+      const int per_pair = a.num_seqs * H;
+      seq = worker % per_pair / H;
+      pair = pairs - 1 - worker / per_pair;
+      step = pairs;
+    } else {
+      const int place = worker / H;
+      seq = seq_of_place(a.query_start_loc, a.num_seqs, 1, kPairShift, place);
+      pair = (int)(place - first_place(a.query_start_loc, seq, 1, kPairShift));
+      step = 0x7fffffff;
+      // there are at least as many CTAs as sequences: each looks one over
+      if (tid == 0 && worker < a.num_seqs) seq_of(a, worker, a.err);
+    }
+    const Seq x = seq_of(a, seq, pairs && tid == 0 ? a.err : nullptr);
+    if (pair < 0 || pair >= x.pairs) return;  // CTA-uniform, before tensor memory is taken
+    if (!pairs) pair = x.pairs - 1 - pair;
     it.set(a, x, worker % H, pair);
     if (it.ntiles == 0) {
-      // zeros; a sequence with more rows than announced has more items than the grid
-      for (int p = pair; p < x.pairs; p += pairs)
-        for (int i = tid; i < min(kPairRows, x.Q - p * kPairRows) * DN; i += kThreads) {
-          const int64_t orow = (int64_t)(x.q0 + p * kPairRows + i / DN) * H + it.head;
+      // zeros; a sequence with more rows than announced has more items than a grid of pairs
+      for (int64_t p = pair; p < x.pairs; p += step)
+        for (int i = tid; i < min(kPairRows, x.Q - (int)p * kPairRows) * DN; i += kThreads) {
+          const int64_t orow = (x.q0 + p * kPairRows + i / DN) * H + it.head;
           static_cast<T *>(a.out)[orow * DN + i % DN] = Elem<T>::from_f(0.f);
           if (a.lse && i % DN == 0) a.lse[orow] = -INFINITY;
         }
@@ -868,9 +893,16 @@ cudaError_t launch_t(const LatentPrefillArgs &a, int sm_count, cudaStream_t stre
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  const int pairs = split ? 0 : (a.max_query_len + kPairRows - 1) / kPairRows;
-  const int64_t grid = split ? sm_count : (int64_t)pairs * a.num_seqs * a.num_heads;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  // One CTA a (pair of Q tiles, sequence, head), or one a (place, head) where that
+  // leaves many CTAs without an item.  The latter fit a grid: the entry point holds
+  // rows * heads and sequences * heads to 2^30 each.
+  const int64_t places = (int64_t)a.num_q_tokens / kPairRows + a.num_seqs;
+  int pairs = (a.max_query_len + kPairRows - 1) / kPairRows;
+  int64_t grid = (int64_t)pairs * a.num_seqs * a.num_heads;
+  if (split || grid > kMostEmpty * places * a.num_heads || grid > 0x7fffffff) {
+    pairs = 0;
+    grid = split ? sm_count : places * a.num_heads;
+  }
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
