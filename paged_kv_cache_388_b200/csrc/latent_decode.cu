@@ -672,19 +672,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 // is no key to see.  One CTA of 8 warps per (sequence, rows_per_cta rows): a
 // warp a row when there are rows enough to fill the machine, else 2, 4 or 8
 // warps that share a row's pieces and join through shared memory (one long
-// sequence is cut into as many pieces as there are workers).
+// sequence is cut into as many pieces as there are workers).  per_seq: CTAs a
+// sequence, or 0, a CTA a place (see first_place) where most of those would find no
+// row: 256 single rows announced as 256 each, 16 heads, took 595 us by sequence and
+// take 101 by places (96 announced as they are), 2000 rows beside 255 single ones at
+// 128 heads 28.3 and 2.0 ms.
 constexpr int kMergeWarps = 8;
+constexpr int kMostEmpty = 2;  // CTAs by sequence for each by places, at most
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * kMergeWarps)
     latent_merge_kernel(const LatentArgs a, const float *rec, const float *rec_ml, const int *pref,
-                        const Line line, int rows_per_cta) {
+                        const Line line, int rows_per_cta, int per_seq) {
   constexpr int V = R / 128;  // float4 a lane: values lane * 4 + 128 v
   __shared__ float4 so[kMergeWarps][R / 4];
   __shared__ float sm[kMergeWarps], sl[kMergeWarps];
-  const int per_seq = (a.max_query_len * a.num_heads + rows_per_cta - 1) / rows_per_cta;
-  const int s = blockIdx.x / per_seq;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int s;
+  int64_t first, step;  // the CTA's rows: first, first + step, ... and rows_per_cta from each
+  if (per_seq) {
+    s = blockIdx.x / per_seq;
+    first = (int64_t)(blockIdx.x % per_seq) * rows_per_cta;
+    step = (int64_t)per_seq * rows_per_cta;
+  } else {
+    const int shift = 31 - __clz(rows_per_cta);
+    s = seq_of_place(a.query_start_loc, a.num_seqs, a.num_heads, shift, blockIdx.x);
+    first = (int64_t)blockIdx.x - first_place(a.query_start_loc, s, a.num_heads, shift);
+    if (first < 0) return;
+    first <<= shift;
+    step = (int64_t)1 << 31;  // past every row
+  }
   const int total = pref[a.num_seqs], p0 = pref[s];
   const Seq x = seq_of(a, line, s, nullptr);
   const int rows = x.Q * a.num_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -697,8 +714,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   };
   if (x.tiles && owner(p0) == owner(p0 + line.units(x, a.num_heads) - 1)) return;  // written by its worker
   const int share = kMergeWarps / rows_per_cta, group = warp / share, part = warp % share;
-  for (int base = (int)(blockIdx.x % per_seq) * rows_per_cta; base < rows; base += per_seq * rows_per_cta) {
-    const int row = base + group;  // the same for all warps that meet at the barrier below
+  for (int64_t base = first; base < rows; base += step) {
+    const int row = (int)base + group;  // the same for all warps that meet at the barrier below
     if (row >= rows) break;
     const int rt = row / line.nr, r = row % line.nr;
     // units of the row's tiles, and the workers that hold them
@@ -883,11 +900,19 @@ cudaError_t launch_t(const LatentArgs &a, const Plan &p, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.max_query_len * a.num_heads;
   int rows_per_cta = 1;  // 512 CTAs at most, if a warp a row allows it
   while (rows_per_cta < kMergeWarps && a.num_seqs * rows > 512 * (int64_t)rows_per_cta) rows_per_cta *= 2;
-  cfg.gridDim = dim3((unsigned)(a.num_seqs * ((rows + rows_per_cta - 1) / rows_per_cta)));
+  int per_seq = (int)((rows + rows_per_cta - 1) / rows_per_cta);
+  int64_t grid = (int64_t)a.num_seqs * per_seq;
+  const int64_t all = (int64_t)a.num_q_tokens * a.num_heads;
+  if (a.query_start_loc && grid > kMostEmpty * (all / rows_per_cta + a.num_seqs)) {
+    per_seq = 0;
+    for (rows_per_cta = 1; rows_per_cta < kMergeWarps && all > 512 * (int64_t)rows_per_cta;) rows_per_cta *= 2;
+    grid = all / rows_per_cta + a.num_seqs;
+  }
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, latent_merge_kernel<T, R>, a, (const float *)rec, (const float *)ml,
-                            (const int *)pref, p.line, rows_per_cta);
+                            (const int *)pref, p.line, rows_per_cta, per_seq);
 }
 
 template <typename T, int R, int NR>
