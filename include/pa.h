@@ -540,9 +540,11 @@ int pa_latent_write(const void *latent, const void *rope, void *latent_cache,
  *                     aligned; calls whose kernels may overlap (other streams,
  *                     two captured graphs) need one each
  * Device checks: a context length outside [0, max_context_len]
- * (PA_DEVERR_CONTEXT_LEN), more than max_query_len rows or row offsets out of
- * range (PA_DEVERR_QUERY_LEN): the sequence's rows within the tensor are
- * zeros.  A block id outside the pool (PA_DEVERR_BLOCK_ID) zeroes the rows of
+ * (PA_DEVERR_CONTEXT_LEN) or more than max_query_len rows
+ * (PA_DEVERR_QUERY_LEN): the sequence's rows are zeros.  Row offsets out of
+ * range (PA_DEVERR_QUERY_LEN): the sequence is skipped, and where
+ * query_start_loc goes back sequences beside that place may be left unwritten
+ * too.  A block id outside the pool (PA_DEVERR_BLOCK_ID) zeroes the rows of
  * its sequence.
  * Cache rows of keys that only some rows of a sequence see must be finite (a
  * weight of 0 times infinity is NaN); slots past a sequence's context may hold

@@ -77,3 +77,29 @@ def test_more_rows_than_announced_among_many(lib):  # noqa: F811
     assert lib.pa_get_device_error() == lib.PA_DEVERR_QUERY_LEN
     assert torch.all(out[n - 1:n + 199] == 0) and torch.all(lse[n - 1:n + 199] == -math.inf)
     assert torch.all(out[n + 199:] == 7) and torch.all(out[: n - 1].abs().sum(-1) > 0)
+
+
+@pytest.mark.parametrize("pad", [0, 300])
+def test_row_offsets_out_of_range_are_skipped(lib, pad):  # noqa: F811
+    """The sequence whose offsets leave the tensor is left as it was, all others are as ever; offsets that go back are
+    reported, and nothing outside is touched."""
+    n, heads = 60, 8
+    user, cache, q, tables, lens = _batch(n, heads, pad, seed=1)
+    dl = torch.tensor(lens, dtype=torch.int32).cuda()
+    good = torch.arange(n + 1, dtype=torch.int32)
+    most = max(1, pad)
+    want = user.attend(q.cuda(), tables.cuda(), dl, 0.06, query_start_loc=good.cuda(), max_query_len=most)[:n]
+    assert lib.pa_get_device_error() == 0
+    bad = good.clone()
+    bad[-1] = n + pad + 1
+    room = torch.full((n + pad + 8, heads, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = user.attend(q.cuda(), tables.cuda(), dl, 0.06, out=room[:n + pad], query_start_loc=bad.cuda(), max_query_len=most)
+    assert lib.pa_get_device_error() == lib.PA_DEVERR_QUERY_LEN
+    # the line of tiles is cut elsewhere without it: half a step of the result and of each weight
+    assert torch.all((out[:n - 1].float() - want[:n - 1].float()).abs() <= 2.0 ** -6 * want.float().abs().amax())
+    assert torch.all(room[n - 1:] == 7)
+    bad = good.clone()
+    bad[30] = 2
+    user.attend(q.cuda(), tables.cuda(), dl, 0.06, out=room[:n + pad], query_start_loc=bad.cuda(), max_query_len=most)
+    assert lib.pa_get_device_error() == lib.PA_DEVERR_QUERY_LEN
+    assert torch.all(room[n + pad:] == 7)
