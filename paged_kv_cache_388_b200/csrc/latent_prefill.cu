@@ -703,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       T *dst = static_cast<T *>(a.out) + orow * DN;
       const bool write = row < it.ntok, whole = j0 == 0 && it.j1 == it.ntiles;
       const int64_t slot = (int64_t)worker * 2 + (j0 == 0 ? 1 : 0);
-      const float inv = fin && l > 0.f ? 1.f / l : (l != l ? l : 0.f);
+      // an item whose waits ran out has no sum: zeros, and -infinity as lse
+      const float inv = !fin ? 0.f : l > 0.f ? 1.f / l : (l != l ? l : 0.f);
       const bool none = !some || inv == 0.f;  // no visible key
       if (whole || it.ntiles == 0) {
 #pragma unroll 1
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (write && a.lse)
-          a.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l != l ? l : -INFINITY);
+          a.lse[orow] = !fin ? -INFINITY : l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l != l ? l : -INFINITY);
       } else if constexpr (SPLIT) {
         const int64_t rrow = slot * kPairRows + row;
         if (write) rec_ml[rrow] = make_float2(m, fin ? l : -1.f);  // a negative sum marks a failure
