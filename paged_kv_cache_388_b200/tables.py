@@ -6,8 +6,11 @@ loop among them: ``step`` releases, forks and grows all rows in one call and
 hands out the new tokens' slots, copying the blocks that a shared row writes
 into; ``compact`` moves the used blocks to the front of the pool, so that the
 pool's tail can be given back.  Calls on the same tables, captured ones among
-them, must follow one another (one stream, or streams that wait): they update
-the tables and share the object's workspace.
+them, must follow one another (one stream, or streams that wait), since they
+update the tables.  Their workspaces are taken from torch's allocator call by
+call, on the stream of the call.
+
+``step`` takes tables of up to 4096 rows, ``compact`` any number.
 """
 from __future__ import annotations
 
@@ -36,9 +39,7 @@ class DeviceBlockTables:
         self.context_lens = own(context_lens, (num_seqs,), "context_lens")
         self.ref_counts = own(ref_counts, (num_blocks,), "ref_counts")
         self.device = self.block_tables.device
-        # kept with the tables: calls on the same tables follow one another anyway
-        self._ws = torch.empty(_lib.pa_table_workspace_size(num_seqs, max_blocks_per_seq, num_blocks),
-                               dtype=torch.uint8, device=self.device)
+        self._ws_bytes = _lib.pa_table_workspace_size(num_seqs, max_blocks_per_seq, num_blocks)
 
     @classmethod
     def from_allocator(cls, allocator, sids, max_blocks_per_seq, device="cuda"):
@@ -69,7 +70,8 @@ class DeviceBlockTables:
         qsl = t.new_empty(n + 1)
         pairs = t.new_empty((n, 2), dtype=torch.int64)
         _lib._table_step(sizes, t, self.context_lens, self.ref_counts, append, self.block_size,
-                         slots, qsl, pairs, release, fork_src, pools, self._ws, None)
+                         slots, qsl, pairs, release, fork_src, pools, t.new_empty(self._ws_bytes, dtype=torch.uint8),
+                         None)
         return slots, qsl, pairs
 
     def compact(self, pools=()):
@@ -81,5 +83,5 @@ class DeviceBlockTables:
         live = t.new_empty(1)
         moves = t.new_empty((max(1, sizes[2] // 2), 2), dtype=torch.int64)
         _lib._table_compact(sizes, t, self.context_lens, self.ref_counts, self.block_size, live,
-                            moves, pools, self._ws, None)
+                            moves, pools, t.new_empty(self._ws_bytes, dtype=torch.uint8), None)
         return live, moves
