@@ -527,7 +527,10 @@ int pa_latent_write(const void *latent, const void *rope, void *latent_cache,
  *     lse[t][h] = ln sum_j exp(s_j)
  * over the keys j <= L - Q + t.  A row that sees no key is written as zeros,
  * its lse as -inf.  fp32 accumulation; the softmax weights enter the second
- * product in the cache's type.
+ * product rounded once to the cache's type: half a step of each weight, 2^-8 in
+ * bf16 and 2^-11 in f16, relative to sum_j w_j |c_j| at most.  f16 weights below
+ * 2^-21 of the largest are off by 2^-32 of it instead.  Sums and lse take the
+ * weights unrounded.
  *
  *   out               [num_q_tokens][num_heads][latent_dim], dtype
  *   lse               float [num_q_tokens][num_heads], or NULL
@@ -572,7 +575,9 @@ size_t pa_latent_decode_workspace_size(int num_seqs, int max_query_len,
  *     out[t][h] = sum_j softmax(s)_j v_j[h],  lse[t][h] = ln sum_j exp(s_j)
  * over the keys j <= L - Q + t (causal != 0) or all L keys (causal == 0, for a
  * cached prefix attended apart and merged by its lse).  A row that sees no key
- * is written as zeros, its lse as -inf.
+ * is written as zeros, its lse as -inf.  fp32 accumulation; the softmax weights
+ * enter the second product rounded once to dtype, as in pa_latent_decode (where
+ * pa_decode gives bf16 weights two words), sums and lse take them unrounded.
  *
  *   q        [num_q_tokens][num_heads][nope_dim + rope_dim], contiguous
  *   k, v     [num_k_tokens] rows of num_heads heads; k_token_stride,
