@@ -83,7 +83,9 @@ __device__ __forceinline__ void mask_keys(uint32_t (&s)[2][32], int last) {
 }
 
 constexpr int kExtra = 1;       // units an item has beside its tiles
-constexpr int kMinUnits = 3;    // units a worker is worth
+// Units a worker is worth: 1 row of 16 heads over 1024 keys took 20.5 / 22.6 / 26.6
+// us at 2 / 3 / 6, 200 rows over 2048 keys 53 / 49 / 51.
+constexpr int kMinUnits = 3;
 constexpr int kPairRows = kQTiles * kRows, kPairShift = 8;
 static_assert(kPairRows == 1 << kPairShift, "rows of an item");
 // CTAs of the grid of pairs for each of the grid of places, at most.  A CTA
@@ -95,7 +97,15 @@ static_assert(kPairRows == 1 << kPairShift, "rows of an item");
 // first (64 prompts of 128 rows 79 against 82 us, nine of 1000 104 against 109; 32
 // of 1 to 2048, nearly half of the CTAs empty, 414 against 398).
 constexpr int kMostEmpty = 2;
-constexpr int kSplitTokens = 1024;  // keys of all sequences below which no item is cut
+// Keys of all sequences together from which items are cut: records and joining
+// cost about 10 us where a sequence has few rows, 25 to 30 where it has hundreds.
+// Cut / whole, us, 16 heads: 1 row over 512 keys 20.5 / 16.4, 1024 22.5 / 24.6,
+// 2048 24.6 / 38.9, 16384 53 / 256; 200 rows over 1024 37 / 31, 2048 49 / 49, 8192
+// 74 / 168; two sequences of 512 rows over 512 41 / 22.5, 2048 61 / 53, 8192 123 /
+// 174.  The host knows the sum of the keys alone, and a long sequence left whole
+// costs more than short ones cut.
+constexpr int kSplitTokens = 1024, kSplitTokensManyRows = 2048;
+constexpr int kManyRows = 128;  // rows a sequence, on average: more than one Q tile
 
 // A cut item's piece, as its worker leaves it for the joining kernel.
 struct Piece {
@@ -835,7 +845,8 @@ bool make_map3(CUtensorMap *m, const void *p, int width, int heads, int tokens, 
 // sequence can be long enough to be worth it.
 bool splits(int num_seqs, int num_q_tokens, int num_k_tokens, int num_heads, int sm_count) {
   const int64_t most = (int64_t)num_heads * ((int64_t)num_q_tokens / kPairRows + num_seqs);
-  return most < sm_count && num_k_tokens >= kSplitTokens;
+  const bool many = num_q_tokens > (int64_t)kManyRows * num_seqs;
+  return most < sm_count && num_k_tokens >= (many ? kSplitTokensManyRows : kSplitTokens);
 }
 
 struct PrefillWs {

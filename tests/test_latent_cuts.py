@@ -102,3 +102,11 @@ def test_prefill_counts_every_key_once(lib, qs, ks, heads, dn, causal, dtype):
     assert lib.pa_get_device_error() == 0
     limit = torch.cat([torch.arange(n) + m - n + 1 if causal else torch.full((n,), m) for n, m in zip(qs, ks)])
     _check(out, lse, limit, dn, dt)
+
+
+def test_what_is_cut(lib):
+    """Keys are cut, and a workspace asked for, where few rows meet many keys."""
+    need = lib.pa_latent_prefill_workspace_size
+    assert need(1, 1, 1024, 16, 128) > 0 and need(1, 200, 2048, 16, 64) > 0 and need(2, 1024, 16384, 16, 128) > 0
+    assert need(1, 1, 1023, 16, 128) == 0 and need(1, 200, 2047, 16, 128) == 0 and need(2, 1024, 1024, 16, 128) == 0
+    assert need(1, 1, 1 << 20, 148, 128) == 0  # items enough for every SM
