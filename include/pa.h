@@ -498,7 +498,11 @@ size_t pa_decode_shared_prefix_fp8_workspace_size(int num_seqs, int num_heads,
  *
  * Supported by pa_latent_write and pa_latent_decode: latent_dim in {256,
  * 512}, rope_dim 64, block_size in {16, 32, 64}, PA_F16 and PA_BF16, any
- * num_heads.
+ * num_heads.  PA_ERR_UNSUPPORTED from pa_latent_decode beyond 2^30
+ * num_q_tokens * num_heads, 2^30 max_blocks_per_seq * block_size, 2^31
+ * num_blocks * block_size, 2^31 num_seqs * max_query_len * num_heads, and 2^31
+ * tiles of 32 or 64 keys by up to 64 rows, counted as if every sequence had
+ * max_context_len keys and max_query_len rows: announce them closely.
  */
 
 /*
@@ -592,7 +596,9 @@ size_t pa_latent_decode_workspace_size(int num_seqs, int max_query_len,
  *   workspace      >= pa_latent_prefill_workspace_size(...) bytes, 16-byte
  *                  aligned; one each for calls whose kernels may overlap
  * Base pointers and strides are multiples of 16 bytes.  Supported: nope_dim =
- * v_dim in {64, 128}, rope_dim 64, PA_F16 and PA_BF16, scale finite and >= 0.
+ * v_dim in {64, 128}, rope_dim 64, PA_F16 and PA_BF16, scale finite and >= 0,
+ * strides above 0 and below 2^38, num_q_tokens * num_heads and num_seqs *
+ * num_heads up to 2^30.  max_query_len may be loose: it costs little.
  * Device checks: offsets out of range or more than max_query_len rows set
  * PA_DEVERR_QUERY_LEN (a sequence with more rows: zeros; offsets out of range:
  * skipped; where query_start_loc goes back, sequences beside that place may be

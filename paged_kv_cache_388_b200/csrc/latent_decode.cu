@@ -36,7 +36,8 @@
 // ragged sequences of 16 heads and 512 values, 320 MB, take 70 us (4.6 TB/s with
 // the merge, tiles arriving at 7 TB/s in between); beyond that the issue of S (36
 // products a tile, 28 cycles each): 64 sequences of 2048 to 8192 keys and 128
-// heads take 146 us (655 TFLOP/s).  With 256 values a tile's softmax is the
+// heads take 143 us (670 TFLOP/s) at 1965 MHz, 163 (590) in a long run of them,
+// whose clock sinks to about 1800.  With 256 values a tile's softmax is the
 // longest step (1800 cycles for 64 rows x 64 keys).
 #include <limits.h>
 

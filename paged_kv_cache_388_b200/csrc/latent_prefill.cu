@@ -24,7 +24,8 @@
 // a record (sums, maximum, total) per range, which a second kernel joins in the
 // order of the ranges.  For many items the line was slower (256 equal items of
 // 130 tiles, which take two rounds on 148 SMs where 1.73 suffice: 640 us against
-// 590; a batch of nine prompts: 141 against 106): cut items cost their records,
+// 590 at 1965 MHz, 660 in a long run, whose clock the power limit holds at 1750; a
+// batch of nine prompts: 141 against 106): cut items cost their records,
 // and K and V are read at different places at a time.
 //
 // K and V arrive by TMA in chunks of 128 keys x 64 columns (16 KB, the

@@ -11,10 +11,12 @@
 //
 // Each is one cooperative kernel whose phases are parted by grid barriers: the
 // work of a phase is a few microseconds at most, so that launches would cost
-// more than it (as six dependent launches a step of 256 rows took 15 us on the
-// device and 13 us of the host's time).  What one CTA can sum up in less than
-// a barrier takes -- the counts of the pool's chunks, the needs of the rows --
-// every CTA sums up for itself.
+// more than it: as six dependent launches a step of 256 rows took 13 us more of
+// the host's time.  On the device alone the six took 15 us and this kernel takes
+// 18, so that in a captured loop, where the host's time is nil, the barriers cost
+// what the launches save elsewhere (a replay of the six was not measured).  What
+// one CTA can sum up in less than a barrier takes -- the counts of the pool's
+// chunks, the needs of the rows -- every CTA sums up for itself.
 #include <cooperative_groups.h>
 #include <limits.h>
 
